@@ -264,6 +264,105 @@ int mxf4_gemm_variant(int variant, const uint8_t *a_codes, const uint8_t *a_sf,
                       void *out, int out_f32, int64_t M, int64_t N, int64_t K,
                       cudaStream_t stream);
 
+/* ---- few tokens at a time: products, a 4-bit cache, attention over it ----
+ *
+ * The layer's other half when it answers instead of filling a batch (no
+ * counterpart on the pages): the same MXFP4 format and block rule, for
+ * products with up to 32 rows, for a cache of keys and values, and for the
+ * attention that reads it. */
+
+/* A few rows times MXFP4 weights:
+ *   out[m][n] = sum_k x[m][k] * b[n][k]
+ * x bf16 [M][K], rows ldx elements apart (the activation is not quantized);
+ * b the decoded MXFP4 weight exactly as mxf4_gemm takes it (b_codes [N][K/2],
+ * b_sf its scales in the scale-factor layout, kq_sf_bytes(N, K) bytes), so
+ * one copy of a layer's weights serves both.  Sums in fp32; out [M][N] is bf16
+ * (out_f32 == 0, rounded to nearest even) or float32.  Every 32-block of x is
+ * brought to fp16 by a power of two (exact but for elements below 2^-38 of
+ * their block's largest, which are off by at most 2^-40 of it); products are
+ * exact.  Needs 0 <= M <= 32, K a positive multiple of 32, N, K < 2^31; any N;
+ * pointers 16-byte aligned, ldx >= K a multiple of 8 (not read for M = 1); out may not overlap the
+ * inputs.  A scale byte 0xFF makes the outputs it reaches NaN. */
+int mxf4_gemv(const void *x_bf16, int64_t ldx, const uint8_t *b_codes, const uint8_t *b_sf,
+              void *out, int out_f32, int64_t M, int64_t N, int64_t K, cudaStream_t stream);
+
+/* A paged MXFP4 cache of one layer's keys and values.  Page p holds
+ * page_size positions of each of the `heads` kv heads:
+ *   codes  uint8 [num_pages][heads][page_size][head_dim/2]
+ *   scales uint8 [num_pages][heads][page_size][head_dim/32]
+ * packed as everywhere in this header; all four arrays 16-byte aligned.
+ * head_dim 32, 64, 96 or 128; page_size a multiple of 16 up to 2^20;
+ * 1 <= heads <= 65535; num_pages < 2^31. */
+typedef struct {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    int64_t num_pages, heads, page_size, head_dim;
+} mx_cache;
+
+/* The sequences of a call, in device arrays:
+ *   cu_seqlens  int32 [batch + 1]: rows cu[b] .. cu[b+1] of the call's T rows
+ *               are sequence b's, in order; not decreasing.  Rows that belong
+ *               to no sequence (padding behind cu[batch]) are not read, and
+ *               what they would write is left as it was.
+ *   seq_lens    int32 [batch]: each sequence's length with its new tokens,
+ *               which are its last ones: row cu[b] + i is at position
+ *               seq_lens[b] - (cu[b+1] - cu[b]) + i.
+ *   block_table int32 [batch] rows of max_pages entries, table_stride
+ *               entries apart: position p of sequence b is in page
+ *               block_table[b][p / page_size].  An entry outside
+ *               [0, num_pages) is no page.
+ * The values are bounded on the device: a position before 0, behind the
+ * table's row or on no page is skipped.  max_pages * page_size < 2^31. */
+typedef struct {
+    const int32_t *block_table;
+    int64_t table_stride, max_pages;
+    const int32_t *cu_seqlens, *seq_lens;
+    int64_t batch;
+} mx_batch;
+
+/* Quantize the keys and values of T new tokens into the cache, each at its
+ * position, by the block rule above (mx_quantize's for bf16 input,
+ * mx_quantize_f32's for fp32: e.g. keys that kq_transform_f32 transformed).
+ * k, v: bf16 or (in_f32 != 0) float32 [T][heads][head_dim], token and head
+ * strides in elements, so slices of a fused projection do; 16-byte aligned,
+ * strides whole 16-byte pieces.  A block with a value that is not finite is
+ * written as the NaN scale 0xFF with zero codes.  Positions other than the new
+ * tokens' keep their bytes.  Two new tokens at the same place of the pool (two
+ * sequences whose new tokens share a page) are outside the contract: its
+ * blocks then hold either's. */
+int mx_cache_write(const void *k, int64_t k_stride_t, int64_t k_stride_h,
+                   const void *v, int64_t v_stride_t, int64_t v_stride_h, int in_f32,
+                   const mx_cache *cache, const mx_batch *seqs, int64_t T, cudaStream_t stream);
+
+/* Read the cache back: row cu[b] + i of out_k and out_v (bf16, or float32 with
+ * out_f32 != 0; [T][heads][head_dim], 16-byte aligned) is position
+ * starts[b] + i of sequence b (starts int32 [batch], NULL for 0; seq_lens is
+ * not read).  bf16 and fp32 hold every value that mx_cache_write stores
+ * exactly (scale bytes 253 and 254, which it never writes, may give infinity);
+ * a scale byte 0xFF gives NaN.  Positions on no page come out as zeros. */
+int mx_cache_read(const mx_cache *cache, const mx_batch *seqs, const int32_t *starts,
+                  void *out_k, void *out_v, int out_f32, int64_t T, cudaStream_t stream);
+
+/* Attention of each sequence's new tokens over its cached positions, the new
+ * ones (written before) among them:
+ *   out[t][h] = softmax_j(scale * q[t][h] . k[j][h / g]) . v[j][h / g]
+ * with g = heads_q / heads query heads per kv head, j over the positions up to
+ * token t's own (causal != 0) or over all of the sequence's seq_lens[b].
+ * q bf16 [T][heads_q][head_dim] with token and head strides (as for
+ * mx_cache_write); out bf16 [T][heads_q][head_dim], contiguous.  Scores,
+ * maxima and sums in fp32, the probabilities rounded to bf16 for the second
+ * product.  A position on no page is not seen; a row that sees nothing is
+ * zero; what a row does not see does not reach it, NaN or not.  K and V scale
+ * bytes 253 to 255 (mx_cache_write writes none of the first two) read as NaN.
+ * max_new: a bound on the new tokens of any one sequence (T does); it selects
+ * the kernels and changes no result beyond rounding.  workspace:
+ * mx_attention_workspace bytes of device memory, 16-byte aligned, not shared
+ * with another call in flight; its content does not matter. */
+int64_t mx_attention_workspace(int64_t T, int64_t heads_q, int64_t head_dim, int64_t max_new);
+int mx_paged_attention(const void *q_bf16, int64_t q_stride_t, int64_t q_stride_h,
+                       const mx_cache *cache, const mx_batch *seqs, float scale, int causal,
+                       void *out_bf16, int64_t T, int64_t heads_q, int64_t max_new,
+                       void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+
 /* Test export: the fp32 transform y = T x (float32 [M][d]) exactly as the
  * quantizer computes it before the amax, for the transform-accuracy check. */
 int kq_transform_f32(const void *act_bf16, const float *factors, int shared,

@@ -20,6 +20,13 @@ W4A4 consumer (scales in the tensor core's scale-factor layout):
     codes, sf     = kq_quantize_sf(act, factors)         # [M, d/2], [kq_sf_bytes(M, d)] uint8
     wcodes, wsf   = mx_quantize_f32(W_folded, sf_layout=True)
     out           = mxf4_gemm(codes, sf, wcodes, wsf)    # bf16 [M, N] = X W^T, W4A4
+
+A few tokens at a time (a 4-bit layer that answers):
+
+    y   = mxf4_gemv(x, wcodes, wsf)                      # bf16 [M, N], M <= 32, x bf16 as it is
+    mx_cache_write(k, v, *cache, table, cu, lens)        # cache: k and v codes and scales, in pages
+    o   = mx_paged_attention(q, *cache, table, cu, lens) # bf16 [T, heads_q, head_dim]
+    k, v = mx_cache_read(*cache, table, cu_k, rows)      # bf16 [rows, heads, head_dim]
 """
 from __future__ import annotations
 
@@ -34,6 +41,7 @@ __all__ = [
     "kq_transform_f32_variant", "kq_quantize_lu", "fwht_quantize", "kq_inverse_f32", "mx_dequantize", "norm_kq_quantize",
     "KQ_SCALES_ROWMAJOR", "KQ_SCALES_SF", "kq_sf_bytes", "kq_quantize_sf", "mx_quantize_f32", "mx_scales_to_sf",
     "mxf4_gemm", "mxf4_gemm_variant", "norm_kq_quantize_sf", "norm_kq_quantize_variant",
+    "mxf4_gemv", "mx_cache_write", "mx_cache_read", "mx_paged_attention", "mx_attention_workspace",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkroquant.so")
@@ -41,7 +49,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkroquant
 KQ_OK, KQ_ERR_NULL, KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_CUDA, KQ_ERR_VARIANT = 0, -1, -2, -3, -4, -5
 KQ_SCALES_ROWMAJOR, KQ_SCALES_SF = 0, 1
 
-# Entry points and their argument types (p = pointer, i = int, q = int64).
+# Entry points and their argument types (p = pointer, i = int, q = int64, f = float).
 _SIGS = {
     "kq_quantize": "ppppqqp",
     "kq_quantize_shared": "ppppqqp",
@@ -63,6 +71,10 @@ _SIGS = {
     "mx_scales_to_sf": "ppqqp",
     "mxf4_gemm": "pppppiqqqp",
     "mxf4_gemm_variant": "ipppppiqqqp",
+    "mxf4_gemv": "pqpppiqqqp",
+    "mx_cache_write": "pqqpqqippqp",
+    "mx_cache_read": "pppppiqp",
+    "mx_paged_attention": "pqqppfipqqqpqp",
 }
 
 _lib = None
@@ -85,7 +97,7 @@ def lib() -> ctypes.CDLL:
                 f"KroQuant CUDA library not found at {LIB_PATH}; build it with "
                 "`python -m w4a4_mxfp4_post_b200.build` (there is no CPU fallback)")
         L = ctypes.CDLL(LIB_PATH)
-        kinds = {"p": ctypes.c_void_p, "i": ctypes.c_int, "q": ctypes.c_int64}
+        kinds = {"p": ctypes.c_void_p, "i": ctypes.c_int, "q": ctypes.c_int64, "f": ctypes.c_float}
         for name, sig in _SIGS.items():
             fn = getattr(L, name)
             fn.argtypes = [kinds[c] for c in sig]
@@ -106,6 +118,8 @@ def lib() -> ctypes.CDLL:
         L.norm_kq_quantize_variant.restype = ctypes.c_int
         L.kq_sf_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64]
         L.kq_sf_bytes.restype = ctypes.c_int64
+        L.mx_attention_workspace.argtypes = [ctypes.c_int64] * 4
+        L.mx_attention_workspace.restype = ctypes.c_int64
         _lib = L
     return _lib
 
@@ -520,3 +534,186 @@ def norm_kq_quantize_sf(h, gamma, beta, factors, eps=1e-6, shared=False, out_cod
     _call("norm_kq_quantize_sf", h.device, _ptr(h), _ptr(gamma), _ptr(beta), int(gamma.shape[0]), float(eps),
           _ptr(factors), int(bool(shared)), _ptr(out_codes), _ptr(out_sf), M, d, _stream(stream, h.device))
     return out_codes, out_sf
+
+
+def mxf4_gemv(x, b_codes, b_sf, out=None, out_dtype=None, stream=None):
+    """A few rows times MXFP4 weights: out[m, n] = sum_k x[m, k] b[n, k], M <= 32.
+
+    x bf16 [M, K] (rows may be strided), not quantized; b_codes [N, K/2] and b_sf the
+    weight operand of mxf4_gemm; out bf16 (default) or float32 [M, N].
+    """
+    torch = _torch()
+    _need_rows(x, "x", (torch.bfloat16,), 2)
+    M, K = x.shape
+    dev = x.device
+    _need(b_codes, "b_codes", torch.uint8, dev)
+    if b_codes.dim() != 2 or b_codes.shape[1] * 2 != K:
+        raise ValueError(f"b_codes must be [N, {K // 2}], got {tuple(b_codes.shape)}")
+    N = b_codes.shape[0]
+    _need(b_sf, "b_sf", torch.uint8, dev, (kq_sf_bytes(N, K),))
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
+    if out.dtype not in (torch.bfloat16, torch.float32) or (out_dtype is not None and out.dtype != out_dtype):
+        raise TypeError(f"out must be {out_dtype or 'bfloat16 or float32'}, got {out.dtype}")
+    _need(out, "out", out.dtype, dev, (M, N))
+    _call("mxf4_gemv", dev, _ptr(x), x.stride(0) if M > 1 else K, _ptr(b_codes), _ptr(b_sf), _ptr(out),
+          int(out.dtype == torch.float32), M, N, K, _stream(stream, dev))
+    return out
+
+
+class _Cache(ctypes.Structure):
+    """mx_cache of the C header."""
+
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")] + \
+               [(n, ctypes.c_int64) for n in ("num_pages", "heads", "page_size", "head_dim")]
+
+
+class _Batch(ctypes.Structure):
+    """mx_batch of the C header."""
+
+    _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("cu_seqlens", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("batch", ctypes.c_int64)]
+
+
+def _need_rows(t, name, dtypes, dim, device=None, shape=None):
+    """An operand whose last dimension is contiguous and whose others may be strided."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must be {dim}-D, got {tuple(t.shape)}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t
+
+
+def _cache(k_codes, k_scales, v_codes, v_scales):
+    torch = _torch()
+    _need(k_codes, "k_codes", torch.uint8)
+    if k_codes.dim() != 4:
+        raise ValueError("k_codes must be [num_pages, heads, page_size, head_dim / 2]")
+    dev = k_codes.device
+    P, H, S, half = k_codes.shape
+    _need(v_codes, "v_codes", torch.uint8, dev, (P, H, S, half))
+    _need(k_scales, "k_scales", torch.uint8, dev, (P, H, S, half // 16))
+    _need(v_scales, "v_scales", torch.uint8, dev, (P, H, S, half // 16))
+    return _Cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), P, H, S, 2 * half), dev
+
+
+def _batch(block_table, cu_seqlens, seq_lens, device):
+    torch = _torch()
+    _need_rows(block_table, "block_table", (torch.int32,), 2, device)
+    B, pages = block_table.shape
+    _need(cu_seqlens, "cu_seqlens", torch.int32, device, (B + 1,))
+    if seq_lens is not None:
+        _need(seq_lens, "seq_lens", torch.int32, device, (B,))
+    return _Batch(_ptr(block_table), max(block_table.stride(0), pages), pages, _ptr(cu_seqlens), _ptr(seq_lens), B)
+
+
+def mx_cache_write(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, seq_lens, stream=None):
+    """Quantize new tokens' keys and values into a paged MXFP4 cache.
+
+    k, v: bf16 or float32 [T, heads, head_dim], tokens and heads may be strided (slices of a
+    fused projection).  The cache: codes uint8 [pages, heads, page_size, head_dim/2] and
+    scales uint8 [pages, heads, page_size, head_dim/32] of keys and of values.  Sequences:
+    block_table int32 [B, max_pages], cu_seqlens int32 [B+1] (rows of each sequence),
+    seq_lens int32 [B] (lengths with the new tokens, which are the last ones).
+    """
+    torch = _torch()
+    c, dev = _cache(k_codes, k_scales, v_codes, v_scales)
+    b = _batch(block_table, cu_seqlens, seq_lens, dev)
+    if seq_lens is None:
+        raise TypeError("seq_lens must be a torch.Tensor")
+    _need_rows(k, "k", (torch.bfloat16, torch.float32), 3, dev)
+    if tuple(k.shape[1:]) != (c.heads, c.head_dim):
+        raise ValueError(f"k must be [T, {c.heads}, {c.head_dim}], got {tuple(k.shape)}")
+    _need_rows(v, "v", (k.dtype,), 3, dev, k.shape)
+    _call("mx_cache_write", dev, _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1),
+          int(k.dtype == torch.float32), ctypes.addressof(c), ctypes.addressof(b), k.shape[0], _stream(stream, dev))
+
+
+def mx_cache_read(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, rows, starts=None, out_k=None,
+                  out_v=None, out_dtype=None, stream=None):
+    """Positions of a paged MXFP4 cache back as bf16 (default) or float32, keys and values.
+
+    Row cu_seqlens[b] + i of the [rows, heads, head_dim] outputs is position starts[b] + i
+    (starts int32 [B], default zeros) of sequence b.
+    """
+    torch = _torch()
+    c, dev = _cache(k_codes, k_scales, v_codes, v_scales)
+    b = _batch(block_table, cu_seqlens, None, dev)
+    if starts is not None:
+        _need(starts, "starts", torch.int32, dev, (b.batch,))
+    shape = (int(rows), c.heads, c.head_dim)
+    dtype = out_dtype or (out_k.dtype if out_k is not None else torch.bfloat16)
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_k and out_v must be bfloat16 or float32, got {dtype}")
+    out_k = torch.empty(shape, dtype=dtype, device=dev) if out_k is None else out_k
+    out_v = torch.empty(shape, dtype=dtype, device=dev) if out_v is None else out_v
+    _need(out_k, "out_k", dtype, dev, shape)
+    _need(out_v, "out_v", dtype, dev, shape)
+    _call("mx_cache_read", dev, ctypes.addressof(c), ctypes.addressof(b), _ptr(starts), _ptr(out_k), _ptr(out_v),
+          int(dtype == torch.float32), shape[0], _stream(stream, dev))
+    return out_k, out_v
+
+
+def mx_attention_workspace(rows: int, heads_q: int, head_dim: int, max_new: int) -> int:
+    """Bytes of workspace that mx_paged_attention needs for calls of these sizes."""
+    n = lib().mx_attention_workspace(int(rows), int(heads_q), int(head_dim), int(max_new))
+    if n < 0:
+        raise ValueError(f"mx_attention_workspace: bad sizes {rows}, {heads_q}, {head_dim}, {max_new}")
+    return n
+
+
+def mx_paged_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, seq_lens, max_new=None,
+                       scale=None, causal=True, out=None, workspace=None, stream=None):
+    """Attention of each sequence's new tokens over its positions in a paged MXFP4 cache.
+
+    q bf16 [T, heads_q, head_dim] (tokens and heads may be strided); heads_q a multiple of the
+    cache's heads.  The new tokens' keys and values have been written (mx_cache_write).
+    causal: a token sees the positions up to its own, otherwise all seq_lens[b].  scale:
+    default head_dim ** -0.5.  max_new: the most new tokens of any one sequence, if known.
+    out bf16 [T, heads_q, head_dim]; rows of no sequence keep their values.  workspace: uint8
+    tensor of mx_attention_workspace(...) bytes for this call alone; allocated if None.
+    """
+    torch = _torch()
+    c, dev = _cache(k_codes, k_scales, v_codes, v_scales)
+    b = _batch(block_table, cu_seqlens, seq_lens, dev)
+    if seq_lens is None:
+        raise TypeError("seq_lens must be a torch.Tensor")
+    _need_rows(q, "q", (torch.bfloat16,), 3, dev)
+    T, hq, d = q.shape
+    if d != c.head_dim or hq == 0 or c.heads == 0 or hq % c.heads:
+        raise ValueError(f"q must be [T, a multiple of {c.heads}, {c.head_dim}], got {tuple(q.shape)}")
+    max_new = T if max_new is None else int(max_new)
+    scale = d ** -0.5 if scale is None else float(scale)
+    if out is None:
+        out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, dev, (T, hq, d))
+    need = mx_attention_workspace(T, hq, d, max_new)
+    if workspace is None:
+        workspace = _scratch(need, dev, stream)
+    _need(workspace, "workspace", torch.uint8, dev)
+    _call("mx_paged_attention", dev, _ptr(q), q.stride(0), q.stride(1), ctypes.addressof(c), ctypes.addressof(b), scale,
+          int(bool(causal)), _ptr(out), T, hq, max_new, _ptr(workspace), workspace.numel(), _stream(stream, dev))
+    return out
+
+
+def _scratch(nbytes, device, stream):
+    """Memory for one call: of the pool of the stream that the call runs on, so that it is
+    used again only after the call."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)

@@ -1636,6 +1636,9 @@ norm_kq_rows_kernel(const uint4 *__restrict__ h, const float *__restrict__ gamma
 #include "kq_mma.cuh"
 #include "kq_ring.cuh"
 #include "mxf4_gemm.cuh"
+#include "mx_cache.cuh"
+#include "mx_attention.cuh"
+#include "mxf4_gemv.cuh"
 
 // Third form of the fused normalisation + quantizer, for long rows (where the
 // per-column table and whole-row buffers of the single-pass kernel do not
@@ -1956,7 +1959,8 @@ Geometry pinned_geometry(int64_t M, int64_t nb, int64_t target_threads)
 enum KernelId {
     kKqDirect, kKqDirectF32, kKqPacked, kKqPackedF32, kSqPacked, kMxPacked, kFold,
     kKqStaged, kSqStaged, kMxStaged, kKqMma, kKqMmaF32, kKqLu, kFwht, kInverse, kDequant, kNormKq,
-    kKqPackedSf, kMxF32, kMxF32Sf, kSfRelayout, kNormRows, kNormKqSf, kKqRing, kNumKernels
+    kKqPackedSf, kMxF32, kMxF32Sf, kSfRelayout, kNormRows, kNormKqSf, kKqRing,
+    kCacheWrite, kCacheWriteF32, kCacheRead, kCacheReadF32, kNumKernels
 };
 std::atomic<int> g_ctas_per_sm[kNumKernels][kMaxDevices];
 
@@ -2669,11 +2673,82 @@ int norm_launch(const char *fn, const void *h_bf16, const float *gamma, const fl
     return launch_check(fn);
 }
 
+// --- few-token operators: argument checks and launches ------------------------
+
+// Head dimensions of the cache and of attention over it: multiples of 32 (the
+// MXFP4 block) up to 128.
+bool head_dim_ok(int64_t D) { return D == 32 || D == 64 || D == 96 || D == 128; }
+
+// Checks of a cache and a batch that need no pointer; fills `s`.
+int check_seqs(const char *fn, const mx_cache *c, const mx_batch *b, int64_t T, cache::Seqs *s)
+{
+    if (!c || !b) return fail(KQ_ERR_NULL, "%s: NULL pointer argument", fn);
+    if (T < 0 || T >= (int64_t(1) << 31) || b->batch < 0 || b->batch >= (int64_t(1) << 31) - 1)
+        return fail(KQ_ERR_SHAPE, "%s: need 0 <= T, batch < 2^31 (T=%lld, batch=%lld)", fn, (long long)T,
+                    (long long)b->batch);
+    if (!head_dim_ok(c->head_dim))
+        return fail(KQ_ERR_SHAPE, "%s: head_dim must be 32, 64, 96 or 128 (got %lld)", fn, (long long)c->head_dim);
+    if (c->heads < 1 || c->heads > 65535)
+        return fail(KQ_ERR_SHAPE, "%s: need 1 <= heads <= 65535 (got %lld)", fn, (long long)c->heads);
+    if (c->page_size < 16 || c->page_size % 16 != 0 || c->page_size > (1 << 20))
+        return fail(KQ_ERR_SHAPE, "%s: page_size must be a multiple of 16 up to 2^20 (got %lld)", fn,
+                    (long long)c->page_size);
+    if (c->num_pages < 0 || c->num_pages >= (int64_t(1) << 31) || b->max_pages < 0 ||
+        b->max_pages >= (int64_t(1) << 31) || b->max_pages * c->page_size >= (int64_t(1) << 31))
+        return fail(KQ_ERR_SHAPE, "%s: need 0 <= num_pages < 2^31 and 0 <= max_pages * page_size < 2^31 "
+                    "(num_pages=%lld, max_pages=%lld)", fn, (long long)c->num_pages, (long long)b->max_pages);
+    if (b->table_stride < b->max_pages || b->table_stride >= (int64_t(1) << 31))
+        return fail(KQ_ERR_SHAPE, "%s: table_stride is below max_pages", fn);
+    s->table = b->block_table;
+    s->table_stride = b->table_stride;
+    s->cu = b->cu_seqlens;
+    s->len = b->seq_lens;
+    s->B = int(b->batch);
+    s->T = int(T);
+    s->max_pages = int(b->max_pages);
+    s->num_pages = int(c->num_pages);
+    s->page = int(c->page_size);
+    s->heads = int(c->heads);
+    return KQ_OK;
+}
+
+// Pointer checks of the above (calls that have work to do).
+int check_seq_pointers(const char *fn, const mx_cache *c, const mx_batch *b, bool need_lens)
+{
+    if (!b->cu_seqlens || (need_lens && !b->seq_lens) || (b->max_pages > 0 && !b->block_table))
+        return fail(KQ_ERR_NULL, "%s: NULL pointer argument", fn);
+    if (c->num_pages > 0 && (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales))
+        return fail(KQ_ERR_NULL, "%s: NULL pointer argument", fn);
+    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_scales, 16))
+        return fail(KQ_ERR_ALIGN, "%s: the cache's arrays must be 16-byte aligned", fn);
+    if (!aligned(b->block_table, 4) || !aligned(b->cu_seqlens, 4) || !aligned(b->seq_lens, 4))
+        return fail(KQ_ERR_ALIGN, "%s: block_table, cu_seqlens and seq_lens must be 4-byte aligned", fn);
+    return KQ_OK;
+}
+
+// A strided [T][heads][D] operand: strides of a token and a head in elements,
+// each a whole number of 16-byte pieces.
+int check_strided(const char *fn, const char *what, const void *p, int64_t st, int64_t sh, int elem)
+{
+    if (!p) return fail(KQ_ERR_NULL, "%s: NULL pointer argument (%s)", fn, what);
+    if (st < 0 || sh < 0) return fail(KQ_ERR_SHAPE, "%s: strides of %s must not be negative", fn, what);
+    if (!aligned(p, 16) || (st * elem) % 16 != 0 || (sh * elem) % 16 != 0)
+        return fail(KQ_ERR_ALIGN, "%s: %s must be 16-byte aligned with strides of whole 16-byte pieces", fn, what);
+    return KQ_OK;
+}
+
+template <int D>
+int attn_rows_launch(const char *fn, const attn::Args &a, cudaStream_t stream)
+{
+    const int64_t warps = int64_t(a.s.T) * a.hq;
+    const int64_t blocks = (warps * 32 + kThreads - 1) / kThreads;
+    if (blocks >= (int64_t(1) << 31)) return fail(KQ_ERR_SHAPE, "%s: too many rows", fn);
+    launch(attn::rows_kernel<D>, unsigned(blocks), kThreads, 0, stream, a);
+    return launch_check(fn);
+}
+
 }  // namespace
 
-// ---------------------------------------------------------------------------
-// C ABI
-// ---------------------------------------------------------------------------
 extern "C" {
 
 int kq_abi_version(void) { return 1; }
@@ -3067,6 +3142,134 @@ int kq_fold_weights(const float *W, const float *factors, int shared, float *W_o
                                                    reinterpret_cast<const float4 *>(factors), shared ? 1 : 0,
                                                    reinterpret_cast<float4 *>(W_out), N * nb, int(nb), geo.T);
     return launch_check("kq_fold_weights");
+}
+
+int mxf4_gemv(const void *x_bf16, int64_t ldx, const uint8_t *b_codes, const uint8_t *b_sf, void *out, int out_f32,
+              int64_t M, int64_t N, int64_t K, cudaStream_t stream)
+{
+    const char *fn = "mxf4_gemv";
+    if (M < 0 || M > gemv::kMaxRows || N < 0 || K <= 0 || K % kBlk != 0)
+        return fail(KQ_ERR_SHAPE, "%s: need 0 <= M <= %d, N >= 0 and K a positive multiple of 32 "
+                    "(M=%lld, N=%lld, K=%lld); mxf4_gemm takes more rows", fn, gemv::kMaxRows, (long long)M,
+                    (long long)N, (long long)K);
+    if (N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31))
+        return fail(KQ_ERR_SHAPE, "%s: N and K must be below 2^31", fn);
+    if (M > 1 && ldx < K) return fail(KQ_ERR_SHAPE, "%s: ldx is below K (ldx=%lld)", fn, (long long)ldx);
+    if (M == 0 || N == 0) return ok();
+    if (!x_bf16 || !b_codes || !b_sf || !out) return fail(KQ_ERR_NULL, "%s: NULL pointer argument", fn);
+    if (!aligned(x_bf16, 16) || !aligned(b_codes, 16) || !aligned(b_sf, 16) || !aligned(out, 16) ||
+        (M > 1 && ldx % 8 != 0))
+        return fail(KQ_ERR_ALIGN, "%s: every pointer must be 16-byte aligned and ldx a multiple of 8", fn);
+    const int64_t blocks = (M * N * 32 + kThreads - 1) / kThreads;
+    const auto *x = static_cast<const __nv_bfloat16 *>(x_bf16);
+    launch(out_f32 ? gemv::rows_kernel<true> : gemv::rows_kernel<false>, unsigned(blocks), kThreads, 0, stream, x, ldx,
+           b_codes, b_sf, out, int(M), N, int(K));
+    return launch_check(fn);
+}
+
+int mx_cache_write(const void *k, int64_t k_stride_t, int64_t k_stride_h, const void *v, int64_t v_stride_t,
+                   int64_t v_stride_h, int in_f32, const mx_cache *c, const mx_batch *b, int64_t T,
+                   cudaStream_t stream)
+{
+    const char *fn = "mx_cache_write";
+    cache::Seqs s;
+    int rc = check_seqs(fn, c, b, T, &s);
+    if (rc != KQ_OK) return rc;
+    if (T == 0 || b->batch == 0 || c->num_pages == 0 || b->max_pages == 0) return ok();
+    const int elem = in_f32 ? 4 : 2;
+    if ((rc = check_seq_pointers(fn, c, b, true)) != KQ_OK) return rc;
+    if ((rc = check_strided(fn, "k", k, k_stride_t, k_stride_h, elem)) != KQ_OK) return rc;
+    if ((rc = check_strided(fn, "v", v, v_stride_t, v_stride_h, elem)) != KQ_OK) return rc;
+    const int nb = int(c->head_dim / kBlk);
+    const int64_t total = T * 2 * c->heads * nb;
+    auto kern = in_f32 ? cache::write_kernel<true> : cache::write_kernel<false>;
+    int64_t target = 0;
+    if ((rc = resident_threads(in_f32 ? kCacheWriteF32 : kCacheWrite, reinterpret_cast<const void *>(kern), &target)) !=
+        KQ_OK)
+        return rc;
+    const int64_t n = target < total ? target : total;
+    launch(kern, unsigned((n + kThreads - 1) / kThreads), kThreads, 0, stream, k, v, k_stride_t, k_stride_h,
+           v_stride_t, v_stride_h, reinterpret_cast<uint4 *>(c->k_codes), c->k_scales,
+           reinterpret_cast<uint4 *>(c->v_codes), c->v_scales, s, nb);
+    return launch_check(fn);
+}
+
+int mx_cache_read(const mx_cache *c, const mx_batch *b, const int32_t *starts, void *out_k, void *out_v, int out_f32,
+                  int64_t T, cudaStream_t stream)
+{
+    const char *fn = "mx_cache_read";
+    cache::Seqs s;
+    int rc = check_seqs(fn, c, b, T, &s);
+    if (rc != KQ_OK) return rc;
+    if (T == 0 || b->batch == 0) return ok();
+    if ((rc = check_seq_pointers(fn, c, b, false)) != KQ_OK) return rc;
+    if (!out_k || !out_v) return fail(KQ_ERR_NULL, "%s: NULL pointer argument", fn);
+    if (!aligned(out_k, 16) || !aligned(out_v, 16) || !aligned(starts, 4))
+        return fail(KQ_ERR_ALIGN, "%s: out_k and out_v must be 16-byte aligned, starts 4-byte aligned", fn);
+    const int nb = int(c->head_dim / kBlk);
+    const int64_t total = T * 2 * c->heads * nb;
+    auto kern = out_f32 ? cache::read_kernel<true> : cache::read_kernel<false>;
+    int64_t target = 0;
+    if ((rc = resident_threads(out_f32 ? kCacheReadF32 : kCacheRead, reinterpret_cast<const void *>(kern), &target)) !=
+        KQ_OK)
+        return rc;
+    const int64_t n = target < total ? target : total;
+    launch(kern, unsigned((n + kThreads - 1) / kThreads), kThreads, 0, stream,
+           reinterpret_cast<const uint4 *>(c->k_codes), c->k_scales, reinterpret_cast<const uint4 *>(c->v_codes),
+           c->v_scales, starts, out_k, out_v, s, nb);
+    return launch_check(fn);
+}
+
+int64_t mx_attention_workspace(int64_t T, int64_t heads_q, int64_t head_dim, int64_t max_new)
+{
+    if (T < 0 || heads_q < 1 || !head_dim_ok(head_dim) || max_new < 0) return -1;
+    return 0;
+}
+
+int mx_paged_attention(const void *q_bf16, int64_t q_stride_t, int64_t q_stride_h, const mx_cache *c,
+                       const mx_batch *b, float scale, int causal, void *out_bf16, int64_t T, int64_t heads_q,
+                       int64_t max_new, void *workspace, int64_t workspace_bytes, cudaStream_t stream)
+{
+    const char *fn = "mx_paged_attention";
+    cache::Seqs s;
+    int rc = check_seqs(fn, c, b, T, &s);
+    if (rc != KQ_OK) return rc;
+    if (heads_q < 1 || heads_q % c->heads != 0 || heads_q > 65535 * c->heads)
+        return fail(KQ_ERR_SHAPE, "%s: heads_q must be a positive multiple of the cache's heads (%lld, %lld)", fn,
+                    (long long)heads_q, (long long)c->heads);
+    if (max_new < 0) return fail(KQ_ERR_SHAPE, "%s: max_new must not be negative", fn);
+    if (!(std::isfinite(scale))) return fail(KQ_ERR_SHAPE, "%s: scale must be finite", fn);
+    if (T == 0 || b->batch == 0) return ok();
+    if ((rc = check_seq_pointers(fn, c, b, true)) != KQ_OK) return rc;
+    if ((rc = check_strided(fn, "q", q_bf16, q_stride_t, q_stride_h, 2)) != KQ_OK) return rc;
+    if (!out_bf16) return fail(KQ_ERR_NULL, "%s: NULL pointer argument", fn);
+    if (!aligned(out_bf16, 16)) return fail(KQ_ERR_ALIGN, "%s: out must be 16-byte aligned", fn);
+    const int64_t need = mx_attention_workspace(T, heads_q, c->head_dim, max_new);
+    if (workspace_bytes < need)
+        return fail(KQ_ERR_SHAPE, "%s: workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes,
+                    (long long)need);
+    if (need > 0 && !workspace) return fail(KQ_ERR_NULL, "%s: NULL pointer argument (workspace)", fn);
+    if (!aligned(workspace, 16)) return fail(KQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+    attn::Args a;
+    a.q = static_cast<const __nv_bfloat16 *>(q_bf16);
+    a.q_st = q_stride_t;
+    a.q_sh = q_stride_h;
+    a.kc = c->k_codes;
+    a.ks = c->k_scales;
+    a.vc = c->v_codes;
+    a.vs = c->v_scales;
+    a.out = static_cast<__nv_bfloat16 *>(out_bf16);
+    a.scale_log2 = scale * 1.44269504088896340736f;
+    a.causal = causal != 0;
+    a.hq = int(heads_q);
+    a.group = int(heads_q / c->heads);
+    a.s = s;
+    switch (c->head_dim) {
+    case 32: return attn_rows_launch<32>(fn, a, stream);
+    case 64: return attn_rows_launch<64>(fn, a, stream);
+    case 96: return attn_rows_launch<96>(fn, a, stream);
+    default: return attn_rows_launch<128>(fn, a, stream);
+    }
 }
 
 }  // extern "C"
