@@ -2737,6 +2737,87 @@ int check_strided(const char *fn, const char *what, const void *p, int64_t st, i
     return KQ_OK;
 }
 
+// --- the few-row product ---
+struct GemvArgs {
+    const __nv_bfloat16 *x;
+    int64_t ldx;
+    const uint8_t *codes, *sf;
+    void *out;
+    int M, N, K;
+    cudaStream_t stream;
+};
+
+template <int RT, int NT, bool F32>
+std::atomic<int> g_gemv_set[kMaxDevices];
+
+template <int RT, int NT, bool F32>
+int gemv_launch(const char *fn, const GemvArgs &a, int parts, int S)
+{
+    auto k = gemv::mxf4_gemv_kernel<RT, NT, F32>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    if (dev < 0 || dev >= kMaxDevices || !g_gemv_set<RT, NT, F32>[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(gemv::kSmem<NT>));
+        if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        if (dev >= 0 && dev < kMaxDevices) g_gemv_set<RT, NT, F32>[dev].store(1, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(parts * S), 1, 1);
+    cfg.blockDim = dim3(gemv::kWarps * 32, 1, 1);
+    cfg.dynamicSmemBytes = gemv::kSmem<NT>;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(S);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = S > 1 ? 2 : 1;
+    (void)cudaLaunchKernelEx(&cfg, k, a.x, a.ldx, a.codes, a.sf, a.out, a.M, a.N, a.K, S);
+    return launch_check(fn);
+}
+
+// Row tiles per CTA and ranks per cluster.  A CTA's x is 2 M / (17/32 x 16 RT)
+// of the bytes of its weights, so it takes as many rows as leave every SM a CTA
+// (with up to 8 ranks); then the ranks fill the two CTAs per SM that fit at
+// once, with at least one chunk of 256 channels for each warp.
+template <int NT, bool F32>
+int gemv_rows(const char *fn, const GemvArgs &a, int sms)
+{
+    constexpr int kMinRT = NT == 1 ? 1 : NT;                 // the channel groups that a fill of x is made for
+    const int groups = (a.N + 127) / 128, KC = (a.K / 32 + gemv::kChunkBlocks - 1) / gemv::kChunkBlocks;
+    auto ranks = [&](int rt) {
+        const int kg = gemv::kWarps / rt, parts = groups * kg;
+        int S = 1;
+        while (S < 8 && int64_t(parts) * S * 2 <= 2 * sms && KC >= 2 * S * kg) S *= 2;
+        return S;
+    };
+    int rt = 8;
+    while (rt > kMinRT && int64_t(groups) * (gemv::kWarps / rt) * ranks(rt) < sms) rt /= 2;
+    const int parts = groups * (gemv::kWarps / rt), S = ranks(rt);
+    switch (rt) {
+    case 8: return gemv_launch<8, NT, F32>(fn, a, parts, S);
+    case 4: return gemv_launch<4, NT, F32>(fn, a, parts, S);
+    case 2: if constexpr (kMinRT <= 2) return gemv_launch<2, NT, F32>(fn, a, parts, S); break;
+    default: if constexpr (kMinRT <= 1) return gemv_launch<1, NT, F32>(fn, a, parts, S); break;
+    }
+    return fail(KQ_ERR_VARIANT, "%s: no such row tile", fn);
+}
+
+template <bool F32>
+int gemv_dispatch(const char *fn, const GemvArgs &a)
+{
+    int sms = 0;
+    int rc = sm_count(&sms);
+    if (rc != KQ_OK) return rc;
+    if (a.M <= 8) return gemv_rows<1, F32>(fn, a, sms);
+    if (a.M <= 16) return gemv_rows<2, F32>(fn, a, sms);
+    return gemv_rows<4, F32>(fn, a, sms);
+}
+
 template <int D>
 int attn_rows_launch(const char *fn, const attn::Args &a, cudaStream_t stream)
 {
@@ -3160,11 +3241,8 @@ int mxf4_gemv(const void *x_bf16, int64_t ldx, const uint8_t *b_codes, const uin
     if (!aligned(x_bf16, 16) || !aligned(b_codes, 16) || !aligned(b_sf, 16) || !aligned(out, 16) ||
         (M > 1 && ldx % 8 != 0))
         return fail(KQ_ERR_ALIGN, "%s: every pointer must be 16-byte aligned and ldx a multiple of 8", fn);
-    const int64_t blocks = (M * N * 32 + kThreads - 1) / kThreads;
-    const auto *x = static_cast<const __nv_bfloat16 *>(x_bf16);
-    launch(out_f32 ? gemv::rows_kernel<true> : gemv::rows_kernel<false>, unsigned(blocks), kThreads, 0, stream, x, ldx,
-           b_codes, b_sf, out, int(M), N, int(K));
-    return launch_check(fn);
+    const GemvArgs a{static_cast<const __nv_bfloat16 *>(x_bf16), ldx, b_codes, b_sf, out, int(M), int(N), int(K), stream};
+    return out_f32 ? gemv_dispatch<true>(fn, a) : gemv_dispatch<false>(fn, a);
 }
 
 int mx_cache_write(const void *k, int64_t k_stride_t, int64_t k_stride_h, const void *v, int64_t v_stride_t,
