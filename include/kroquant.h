@@ -277,10 +277,10 @@ int mxf4_gemm_variant(int variant, const uint8_t *a_codes, const uint8_t *a_sf,
  * b the decoded MXFP4 weight exactly as mxf4_gemm takes it (b_codes [N][K/2],
  * b_sf its scales in the scale-factor layout, kq_sf_bytes(N, K) bytes), so
  * one copy of a layer's weights serves both.  Sums in fp32; out [M][N] is bf16
- * (out_f32 == 0, rounded to nearest even) or float32.  Every 32-block of x is
- * brought to fp16 by a power of two (exact but for elements below 2^-38 of
- * their block's largest, which are off by at most 2^-40 of it); products are
- * exact.  Needs 0 <= M <= 32, K a positive multiple of 32, N, K < 2^31; any N;
+ * (out_f32 == 0, rounded to nearest even) or float32.  Every 256 channels of a
+ * row of x are brought to fp16 by a power of two (exact but for elements below
+ * 2^-32 of the largest of them, which are off by at most 2^-40 of it); products
+ * are exact.  Needs 0 <= M <= 32, K a positive multiple of 32, N, K < 2^31; any N;
  * pointers 16-byte aligned, ldx >= K a multiple of 8 (not read for M = 1); out may not overlap the
  * inputs.  A scale byte 0xFF makes the outputs it reaches NaN. */
 int mxf4_gemv(const void *x_bf16, int64_t ldx, const uint8_t *b_codes, const uint8_t *b_sf,

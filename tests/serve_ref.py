@@ -32,22 +32,25 @@ def sf_of(scales, fill=0xFF):
 
 
 def gemv(x, codes, scales):
-    """(product, sum of |x b|, sum over blocks of max|x| times sum |b|) in float64."""
+    """(product, sum of |x b|, sum over chunks of 256 of max|x| times sum |b|) in float64."""
     b, xd = decode(codes, scales), x.double()
     bad = torch.isnan(b).any()
     y = xd @ b.T
-    xb, bb = xd.abs().unflatten(-1, (-1, 32)), b.abs().unflatten(-1, (-1, 32))
-    if bad:
-        bb = torch.nan_to_num(bb)
-    return y, xd.abs() @ bb.flatten(-2).T, xb.amax(-1) @ bb.sum(-1).T
+    bb = torch.nan_to_num(b).abs() if bad else b.abs()
+    pad = (0, -b.shape[1] % 256)
+    xc = torch.nn.functional.pad(xd.abs(), pad).unflatten(-1, (-1, 256))
+    bc = torch.nn.functional.pad(bb, pad).unflatten(-1, (-1, 256))
+    return y, xd.abs() @ bb.T, xc.amax(-1) @ bc.sum(-1).T
 
 
 def gemv_bound(y, ab, tail, K, bf16):
     """K exact products summed in fp32 in any order, each add off by at most
     2^-23 of the running sum of magnitudes (covers truncating adds), and the
     block scalings (exact, or off by 2^-23 of a block's sum near the ends of
-    fp32: two more such units); an element of x below 2^-38 of its block's
-    largest is off by 2^-40 of that.  bf16 output: half a step of the value."""
+    fp32: two more such units); an element of x below 2^-32 of the largest of
+    its 256 channels is off by 2^-40 of that: the largest is 2^15 or more in
+    fp16, whose subnormals have steps of 2^-24.  bf16 output: half a step of
+    the value."""
     tol = (K + 2) * 2.0 ** -23 * ab + 2.0 ** -40 * tail
     return tol + BF16 * (y.abs() + tol) if bf16 else tol
 

@@ -17,13 +17,13 @@
 // (The legacy MMA is enough: 8 clocks for 16 x 16 weights, a quarter of what
 // their bytes take; a tcgen05 MMA would need the codes in shared memory.)
 // The two MMAs of a 32-block run into a zero accumulator, which is then added
-// to the sum with the block's two scales, in fp32:
-//   sum[n][m] += (codes . x') * (2^(sb[n] - 127) * 2^ex[m])
-// where x' = x 2^-ex is the block of x brought to fp16 by a power of two that
-// puts its largest element in [2^14, 2^15): exact for bf16's 8 bits unless an
-// element is below 2^-38 of the largest (then off by at most 2^-40 of it, the
-// step of fp16's subnormals).  Blockwise, so that one loud channel costs no
-// other block its bits.
+// to the chunk's sum with the block's scale, and the chunk's to the whole, in
+// fp32:
+//   chunk[n][m] += (codes . x') * 2^(sb[n] - 127),   sum[n][m] += chunk[n][m] * 2^ex[m]
+// where x' = x 2^-ex is a chunk (256 channels) of x brought to fp16 by a power
+// of two that puts its largest element in [2^15, 2^16): bf16's 8 bits stay
+// exact down to 2^-32 of the largest; what is below is off by at most 2^-40 of
+// it, half the step of fp16's subnormals.
 //
 // Layout.  A warp owns a tile of 16 weight rows: 4 consecutive lanes l of a
 // 128-row scale group and their 4 quarters (rows base + 32 q + l), so that its
@@ -32,7 +32,7 @@
 // the warp's own ring of kStages (nothing but the warp waits for it), the
 // 16-byte pieces xor-swizzled by row, so that the 4-byte reads of 8 rows x 4
 // words are conflict-free.  A CTA is 8 warps: RT row tiles x 8 / RT groups of
-// channels; x is converted once per CTA for `kXBlocks` blocks at a time and
+// channels; x is converted once per CTA for `kXChunks` chunks at a time and
 // shared by all warps.  The channels are also split over the CTAs of a
 // cluster (up to 8), whose partial sums are added through distributed shared
 // memory in rank order: one launch, no workspace, the same bits every time.
@@ -49,17 +49,23 @@ constexpr int kStageBytes = kCodeBytes + kScaleBytes;
 constexpr int kTableBytes = 16 * kChunkBlocks * 4;            // decoded scales of the current stage
 constexpr size_t kRing = size_t(kWarps) * (kStages * kStageBytes + kTableBytes);
 
-// Blocks of x held at once: 32 KB of fp16 whatever the number of rows.
+// Chunks of x held at once: 32 KB of fp16 whatever the number of rows.  A
+// block's rows are 64 bytes each, and 64 bytes of padding put two consecutive
+// blocks of a row into different halves of the banks.
 template <int NT>
-constexpr int kXBlocks = 64 / NT;
+constexpr int kXChunks = 8 / NT;
+template <int NT>
+constexpr int kXBlockBytes = 8 * NT * 64 + 64;
+template <int NT>
+constexpr int kXBytes = kXChunks<NT> * kChunkBlocks * kXBlockBytes<NT>;
 
 template <int NT>
-constexpr size_t kSmem = kRing + size_t(kXBlocks<NT>) * 8 * NT * (64 + 4);
+constexpr size_t kSmem = kRing + size_t(kXBytes<NT>) + size_t(kXChunks<NT>) * 8 * NT * 4;
 
-// Copy 16 bytes if `full`, else write zeros (src is not read then).
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool full)
+// Copy `bytes` (16, or 0: src is not read) and fill up 16 bytes with zeros.
+__device__ __forceinline__ void cp_async16_sized(uint32_t dst, const void *src, uint32_t bytes)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(full ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -99,37 +105,47 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// A block of x as fp16 scaled by 2^-ex into dst (64 bytes); returns 2^ex.  The
-// exponent is that of the largest finite element, so an infinity stays one
-// and leaves the others their values.
-__device__ __forceinline__ float x_block(const uint4 (&raw)[4], uint4 *dst)
+// 8 elements of a chunk of x (the warp holds its 256) as fp16 scaled by 2^-ex;
+// e = 2^ex.  The exponent is that of the largest finite element, so an
+// infinity stays one and leaves the others their values.
+__device__ __forceinline__ uint4 x_chunk(const uint4 raw, float &e)
 {
-    float v[32];
-    unpack32(raw, v);
-    float top = 0.0f;
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    // magnitudes as 16-bit patterns, which order like the numbers
+    uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    top = __reduce_max_sync(0xffffffffu, max(top << 16, top & 0xffff0000u));
+    if (top >= 0x7f800000u) {
+        top = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float a = fabsf(v[i]);
-        top = fmaxf(top, a <= 3.40282347e38f ? a : 0.0f);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = (w[i] << 16) & 0x7fff0000u, hi = w[i] & 0x7fff0000u;
+            top = max(top, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
     }
-    // biased exponent of 2^ex: the largest element's less 14; at least 1 (2^-126:
+    // biased exponent of 2^ex: the largest element's less 15; at least 1 (2^-126:
     // bf16's subnormals are then multiples of 2^-7 and exact in fp16)
-    const int field = max(int(__float_as_uint(top) >> 23) - 14, 1);
+    const int field = max(int(top >> 23) - 15, 1);
     const float down = __uint_as_float(uint32_t(254 - field) << 23);
+    e = __uint_as_float(uint32_t(field) << 23);
+    uint32_t h[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        dst[q] = make_uint4(pack_f16x2(v[8 * q] * down, v[8 * q + 1] * down),
-                            pack_f16x2(v[8 * q + 2] * down, v[8 * q + 3] * down),
-                            pack_f16x2(v[8 * q + 4] * down, v[8 * q + 5] * down),
-                            pack_f16x2(v[8 * q + 6] * down, v[8 * q + 7] * down));
-    return __uint_as_float(uint32_t(field) << 23);
+    for (int i = 0; i < 4; ++i) h[i] = pack_f16x2(bf16_lo(w[i]) * down, bf16_hi(w[i]) * down);
+    return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-__device__ __forceinline__ uint32_t cluster_rank()
+// Four scale bytes as their values: the byte is the exponent field of 2^(byte -
+// 127), but for 0 (the subnormal 2^-127) and 255 (NaN).
+__device__ __forceinline__ float4 scales4(uint32_t w)
 {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = max(__byte_perm(w, 0, 0x0444 | (i << 12)) >> 1, 0x00400000u);
+    if ((~w - 0x01010101u) & w & 0x80808080u) {               // some byte is 255
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] |= v[i] == 0x7f800000u ? 0x00400000u : 0u;
+    }
+    return make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
 }
 
 __device__ __forceinline__ void cluster_sync()
@@ -158,46 +174,54 @@ mxf4_gemv_kernel(const __nv_bfloat16 *__restrict__ x, int64_t ldx, const uint8_t
     pdl_wait();
     constexpr int KG = kWarps / RT;                           // channel groups
     constexpr int kLanes = 4 * RT;                            // lanes l of the scale group per CTA
-    constexpr int XB = kXBlocks<NT>;
+    constexpr int XC = kXChunks<NT>;
     constexpr int kRows = 16 * RT;
-    static_assert(XB % (kChunkBlocks * KG) == 0, "a fill of x is whole rounds of the channel groups");
+    static_assert(XC % KG == 0, "a fill of x is whole rounds of the channel groups");
     extern __shared__ __align__(16) uint8_t smem_dyn[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = lane / 4, c = lane % 4;
     const int rt = warp % RT, kg = warp / RT;
     uint8_t *ring = smem_dyn + warp * (kStages * kStageBytes + kTableBytes);
     float4 *table = reinterpret_cast<float4 *>(ring + kStages * kStageBytes);
-    uint4 *xs = reinterpret_cast<uint4 *>(smem_dyn + kRing);  // [XB][8 NT][64 bytes]
-    float *xe = reinterpret_cast<float *>(smem_dyn + kRing + size_t(XB) * 8 * NT * 64);   // [XB][8 NT]
+    uint8_t *xs = smem_dyn + kRing;                           // [blocks][8 NT rows of 64 bytes, padding]
+    float *xe = reinterpret_cast<float *>(xs + kXBytes<NT>);  // [XC][8 NT]
 
     const int part = int(blockIdx.x) / S, rank = int(blockIdx.x) % S;
     const int group = part / KG, l0 = (part % KG) * kLanes + 4 * rt;       // the warp's lanes: l0 .. l0 + 3
     const int nb = K / 32, Ka = (nb + 3) / 4, KC = (nb + kChunkBlocks - 1) / kChunkBlocks;
     const int c0 = int(int64_t(rank) * KC / S), c1 = int(int64_t(rank + 1) * KC / S);
 
-    // this lane's pieces of a stage: rows (lane / 8) + 4 j (= lane l0 + lane / 8, quarter j), piece lane % 8
+    // this lane's pieces of a stage: rows (lane / 8) + 4 j (lane l0 + lane / 8 of
+    // the group, quarter j), piece lane % 8; rows past N are zeros
     const int piece = lane % 8;
     const int n0 = group * 128 + l0 + lane / 8;
-    const uint8_t *src = codes + int64_t(n0) * (K / 2) + piece * 16;
-    const uint8_t *ssrc = sf + int64_t(group) * Ka * 512 + (lane / 4) * 512 + l0 * 16 + (lane % 4) * 16;
+    const uint8_t *src[4];
+    uint32_t size[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        size[j] = n0 + 32 * j < N ? 16 : 0;
+        src[j] = codes + int64_t(min(n0 + 32 * j, N - 1)) * (K / 2) + int64_t(c0 + kg) * 128 + piece * 16;
+    }
+    const uint8_t *ssrc = sf + (int64_t(group) * Ka + 2 * (c0 + kg) + (lane / 4) % 2) * 512 + l0 * 16 + (lane % 4) * 16;
     const uint32_t ring_s = smem_addr(ring);
+    const uint32_t dst0 = ring_s + (lane / 8) * 128 + ((piece ^ (lane / 8)) << 4);
+    const uint32_t dst1 = ring_s + (lane / 8) * 128 + ((piece ^ (lane / 8 + 4)) << 4);
 
-    // stage `slot` <- chunk ch (or nothing past the rank's last)
+    // stage `slot` <- chunk ch, the warp's next (or nothing past the rank's last)
     auto fetch = [&](int ch, int slot) {
         if (ch < c1) {
-            const uint32_t dst = ring_s + slot * kStageBytes;
+            const uint32_t at = slot * kStageBytes;
             const bool in_k = ch * kChunkBlocks + piece < nb;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int row = 4 * j + lane / 8;
-                const bool full = in_k && n0 + 32 * j < N;
-                cp_async16_or_zero(dst + row * 128 + ((piece ^ (row & 7)) << 4),
-                                   full ? src + int64_t(32 * j) * (K / 2) + int64_t(ch) * 128 : codes, full);
+                cp_async16_sized((j % 2 ? dst1 : dst0) + at + j * 512, in_k ? src[j] : codes, in_k ? size[j] : 0);
+                src[j] += KG * 128;
             }
             if (lane < 8) {
-                const bool full = 2 * ch + lane / 4 < Ka;
-                cp_async16_or_zero(dst + kCodeBytes + lane * 16, full ? ssrc + int64_t(ch) * 1024 : sf, full);
+                const bool in_a = 2 * ch + lane / 4 < Ka;
+                cp_async16_sized(ring_s + at + kCodeBytes + lane * 16, in_a ? ssrc : sf, in_a ? 16 : 0);
             }
+            ssrc += KG * 1024;
         }
         cp_commit();
     };
@@ -210,27 +234,30 @@ mxf4_gemv_kernel(const __nv_bfloat16 *__restrict__ x, int64_t ldx, const uint8_t
 
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch(c0 + i * KG + kg, i);
+    // columns of no row stay zero
+    for (int i = threadIdx.x; i < XC * kChunkBlocks * 8 * NT * 4; i += kWarps * 32) {
+        const int m = i / 4 % (8 * NT), j = i / (32 * NT);
+        if (m >= M) *reinterpret_cast<uint4 *>(xs + j * kXBlockBytes<NT> + m * 64 + (i % 4) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (threadIdx.x < XC * 8 * NT) xe[threadIdx.x] = 0.0f;
     int it = 0;
-    for (int f0 = c0; f0 < c1; f0 += XB / kChunkBlocks) {
-        // ---- x of the next XB blocks: fp16 and the powers of two
+    for (int f0 = c0; f0 < c1; f0 += XC) {
+        // ---- the next XC chunks of x, a row's chunk per warp and turn
         __syncthreads();
-        const int blocks = min(XB, nb - f0 * kChunkBlocks);
-        for (int i = threadIdx.x; i < XB * 8 * NT; i += kWarps * 32) {
-            const int j = i % XB, m = i / XB;                 // consecutive threads: consecutive blocks of a row
-            uint4 *dst = xs + (j * 8 * NT + m) * 4;
-            float s = 0.0f;
-            if (m < M && j < blocks) {
-                uint4 raw[4];
-                load_block(reinterpret_cast<const uint4 *>(x + m * ldx + int64_t(f0 * kChunkBlocks + j) * 32), 0, raw);
-                s = x_block(raw, dst);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) dst[q] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            xe[j * 8 * NT + m] = s;
+#pragma unroll 4
+        for (int i = warp; i < XC * M; i += kWarps) {
+            const int cc = i % XC, m = i / XC, blk = (f0 + cc) * kChunkBlocks + lane / 4;
+            if ((f0 + cc) * kChunkBlocks >= nb) continue;
+            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+            if (blk < nb)
+                raw = __ldg(reinterpret_cast<const uint4 *>(x + m * ldx + int64_t(blk) * 32 + (lane % 4) * 8));
+            float e;
+            const uint4 h = x_chunk(raw, e);
+            *reinterpret_cast<uint4 *>(xs + (cc * kChunkBlocks + lane / 4) * kXBlockBytes<NT> + m * 64 + (lane % 4) * 16) = h;
+            if (lane == 0) xe[cc * 8 * NT + m] = e;
         }
         __syncthreads();
-        const int f1 = min(c1, f0 + XB / kChunkBlocks);
+        const int f1 = min(c1, f0 + XC);
         for (int ch = f0 + kg; ch < f1; ch += KG, ++it) {
             cp_wait<kStages - 2>();
             __syncwarp();
@@ -239,17 +266,23 @@ mxf4_gemv_kernel(const __nv_bfloat16 *__restrict__ x, int64_t ldx, const uint8_t
             {
                 // the stage's 128 scales as floats, [unit][row][4]: lane = unit * 16 + (l * 4 + quarter)
                 const uint32_t w = reinterpret_cast<const uint32_t *>(st + kCodeBytes)[lane];
-                const int blk = ch * kChunkBlocks + (lane / 16) * 4;
-                float4 s;
-                s.x = blk < nb ? e8m0_value(w & 0xFFu) : 0.0f;
-                s.y = blk + 1 < nb ? e8m0_value((w >> 8) & 0xFFu) : 0.0f;
-                s.z = blk + 2 < nb ? e8m0_value((w >> 16) & 0xFFu) : 0.0f;
-                s.w = blk + 3 < nb ? e8m0_value(w >> 24) : 0.0f;
+                float4 s = scales4(w);
+                const int left = nb - (ch * kChunkBlocks + (lane / 16) * 4);
+                if (left < 4) {                               // padding bytes of the last unit may hold anything
+                    if (left < 1) s.x = 0.0f;
+                    if (left < 2) s.y = 0.0f;
+                    if (left < 3) s.z = 0.0f;
+                    s.w = 0.0f;
+                }
                 table[(lane & 16) + (lane & 3) * 4 + ((lane >> 2) & 3)] = s;
             }
             __syncwarp();
-            const uint4 *xc = xs + ((ch - f0) * kChunkBlocks * 8 * NT + g) * 4 + c;
-            const float *xf = xe + (ch - f0) * kChunkBlocks * 8 * NT + 2 * c;
+            const uint8_t *xc = xs + (ch - f0) * kChunkBlocks * kXBlockBytes<NT> + g * 64 + c * 16;
+            float sum[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[t][i] = 0.0f;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const float4 t0 = table[u * 16 + g], t1 = table[u * 16 + g + 8];
@@ -263,17 +296,24 @@ mxf4_gemv_kernel(const __nv_bfloat16 *__restrict__ x, int64_t ldx, const uint8_t
                     codes_f16(*reinterpret_cast<const uint32_t *>(row + 8 * 128), d);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        const uint4 bx = xc[(j * NT + t) * 32];
-                        const float2 e = *reinterpret_cast<const float2 *>(xf + (j * NT + t) * 8);
+                        const uint4 bx = *reinterpret_cast<const uint4 *>(xc + j * kXBlockBytes<NT> + t * 512);
                         float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                         mma_f16(p, a[0], d[0], a[1], d[1], bx.x, bx.y);
                         mma_f16(p, a[2], d[2], a[3], d[3], bx.z, bx.w);
-                        acc[t][0] = fmaf(p[0], lo[b] * e.x, acc[t][0]);
-                        acc[t][1] = fmaf(p[1], lo[b] * e.y, acc[t][1]);
-                        acc[t][2] = fmaf(p[2], hi[b] * e.x, acc[t][2]);
-                        acc[t][3] = fmaf(p[3], hi[b] * e.y, acc[t][3]);
+                        sum[t][0] = fmaf(p[0], lo[b], sum[t][0]);
+                        sum[t][1] = fmaf(p[1], lo[b], sum[t][1]);
+                        sum[t][2] = fmaf(p[2], hi[b], sum[t][2]);
+                        sum[t][3] = fmaf(p[3], hi[b], sum[t][3]);
                     }
                 }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const float2 e = *reinterpret_cast<const float2 *>(xe + (ch - f0) * 8 * NT + 8 * t + 2 * c);
+                acc[t][0] = fmaf(sum[t][0], e.x, acc[t][0]);
+                acc[t][1] = fmaf(sum[t][1], e.y, acc[t][1]);
+                acc[t][2] = fmaf(sum[t][2], e.x, acc[t][2]);
+                acc[t][3] = fmaf(sum[t][3], e.y, acc[t][3]);
             }
         }
     }
