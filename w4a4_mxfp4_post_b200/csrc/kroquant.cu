@@ -1637,8 +1637,8 @@ norm_kq_rows_kernel(const uint4 *__restrict__ h, const float *__restrict__ gamma
 #include "kq_ring.cuh"
 #include "mxf4_gemm.cuh"
 #include "mx_cache.cuh"
-#include "mx_attention.cuh"
 #include "mxf4_gemv.cuh"
+#include "mx_attention.cuh"
 
 // Third form of the fused normalisation + quantizer, for long rows (where the
 // per-column table and whole-row buffers of the single-pass kernel do not
@@ -2818,14 +2818,46 @@ int gemv_dispatch(const char *fn, const GemvArgs &a)
     return gemv_rows<4, F32>(fn, a, sms);
 }
 
-template <int D>
-int attn_rows_launch(const char *fn, const attn::Args &a, cudaStream_t stream)
+// --- attention over the cache ---
+template <class C>
+std::atomic<int> g_few_ctas[kMaxDevices];
+
+// The few-rows kernel on a grid that fills the device once, then the merge.
+template <class C>
+int few_launch(const char *fn, const attn::Args &a, cudaStream_t stream)
 {
-    const int64_t warps = int64_t(a.s.T) * a.hq;
-    const int64_t blocks = (warps * 32 + kThreads - 1) / kThreads;
-    if (blocks >= (int64_t(1) << 31)) return fail(KQ_ERR_SHAPE, "%s: too many rows", fn);
-    launch(attn::rows_kernel<D>, unsigned(blocks), kThreads, 0, stream, a);
+    auto k = attn::few_kernel<C>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    int ctas = dev >= 0 && dev < kMaxDevices ? g_few_ctas<C>[dev].load(std::memory_order_acquire) : 0;
+    if (ctas <= 0) {
+        int sms = 0, per = 0;
+        const int rc = sm_count(&sms);
+        if (rc != KQ_OK) return rc;
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k, C::kWarps * 32, C::kSmem);
+        if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "occupancy query: %s", cudaGetErrorString(e));
+        ctas = sms * (per < 1 ? 1 : per);
+        if (ctas > attn::kMaxCtas) ctas = attn::kMaxCtas;
+        if (dev >= 0 && dev < kMaxDevices) g_few_ctas<C>[dev].store(ctas, std::memory_order_release);
+    }
+    launch(k, unsigned(ctas), C::kWarps * 32, C::kSmem, stream, a);
+    const int rc = launch_check(fn);
+    if (rc != KQ_OK) return rc;
+    launch(attn::merge_kernel<C::R, C::D, 256>, unsigned(ctas), 256, 0, stream, a);
     return launch_check(fn);
+}
+
+template <int D>
+int attn_launch(const char *fn, attn::Args a, int64_t max_new, cudaStream_t stream)
+{
+    (void)max_new;
+    a.rows_lo = 0;
+    a.rows_hi = INT32_MAX;
+    if (max_new * a.group <= 8) return few_launch<attn::Few<D, 1>>(fn, a, stream);
+    return few_launch<attn::Few<D, 2>>(fn, a, stream);
 }
 
 }  // namespace
@@ -3301,7 +3333,7 @@ int mx_cache_read(const mx_cache *c, const mx_batch *b, const int32_t *starts, v
 int64_t mx_attention_workspace(int64_t T, int64_t heads_q, int64_t head_dim, int64_t max_new)
 {
     if (T < 0 || heads_q < 1 || !head_dim_ok(head_dim) || max_new < 0) return -1;
-    return 0;
+    return attn::kMaxCtas * (int64_t(sizeof(attn::Desc)) + 2 * 16 * (head_dim + 2) * 4);
 }
 
 int mx_paged_attention(const void *q_bf16, int64_t q_stride_t, int64_t q_stride_h, const mx_cache *c,
@@ -3342,11 +3374,16 @@ int mx_paged_attention(const void *q_bf16, int64_t q_stride_t, int64_t q_stride_
     a.hq = int(heads_q);
     a.group = int(heads_q / c->heads);
     a.s = s;
+    a.page_shift = -1;
+    for (int i = 4; i <= 20; ++i)
+        if (c->page_size == int64_t(1) << i) a.page_shift = i;
+    a.work = static_cast<uint8_t *>(workspace);
+    const int64_t most = max_new < T ? max_new : T;
     switch (c->head_dim) {
-    case 32: return attn_rows_launch<32>(fn, a, stream);
-    case 64: return attn_rows_launch<64>(fn, a, stream);
-    case 96: return attn_rows_launch<96>(fn, a, stream);
-    default: return attn_rows_launch<128>(fn, a, stream);
+    case 32: return attn_launch<32>(fn, a, most, stream);
+    case 64: return attn_launch<64>(fn, a, most, stream);
+    case 96: return attn_launch<96>(fn, a, most, stream);
+    default: return attn_launch<128>(fn, a, most, stream);
     }
 }
 
