@@ -357,7 +357,7 @@ int mx_cache_read(const mx_cache *cache, const mx_batch *seqs, const int32_t *st
  * the kernels and changes no result beyond rounding.  workspace:
  * mx_attention_workspace bytes of device memory, 16-byte aligned, not shared
  * with another call in flight; its content does not matter. */
-int64_t mx_attention_workspace(int64_t T, int64_t heads_q, int64_t head_dim, int64_t max_new);
+int64_t mx_attention_workspace(int64_t T, int64_t heads_q, int64_t heads, int64_t head_dim, int64_t max_new);
 int mx_paged_attention(const void *q_bf16, int64_t q_stride_t, int64_t q_stride_h,
                        const mx_cache *cache, const mx_batch *seqs, float scale, int causal,
                        void *out_bf16, int64_t T, int64_t heads_q, int64_t max_new,

@@ -622,3 +622,11 @@ def test_a_layer_answers_token_by_token(cuda_device, transformed):
         want, ab, tail = ref.gemv(o.view(T, hq * d), w, ws)
         assert ((y.double() - want).abs() <= ref.gemv_bound(want, ab, tail, hq * d, False)).all()
     assert kq.kq_wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("hkv,new", [(8, 32), (40, 20), (8, 70), (3, 150)])
+def test_attention_items_of_one_and_two_tiles_in_turn(cuda_device, hkv, new):
+    """Many heads whose rows end in a half-filled item, long contexts beside short ones: no wait of the kernels runs out."""
+    p = Plan([1500, 0, 130], [new, new, new // 2], hkv, 64, 16, seed=70)
+    attend(p, normal(p.T, 4 * hkv, 64, key=70), max_new=new)
+    assert kq.kq_wait_timeouts() == 0

@@ -109,9 +109,11 @@ def test_attention_refusals(L):
     assert attend(L, cache(), batch(), q=None) == -1 and attend(L, cache(), batch(), o=None) == -1
     assert attend(L, cache(), batch(), q=8) == -3 and attend(L, cache(), batch(), o=8) == -3
     assert attend(L, cache(), batch(), st=252) == -3 and attend(L, cache(), batch(), sh=-64) == -2
-    assert L.mx_attention_workspace(4, 4, 64, 1) >= 0
-    assert L.mx_attention_workspace(-1, 4, 64, 1) == -1 and L.mx_attention_workspace(4, 0, 64, 1) == -1
-    assert L.mx_attention_workspace(4, 4, 48, 1) == -1 and L.mx_attention_workspace(4, 4, 64, -1) == -1
+    assert L.mx_attention_workspace(4, 4, 2, 64, 1) >= 0
+    assert L.mx_attention_workspace(-1, 4, 2, 64, 1) == -1 and L.mx_attention_workspace(4, 0, 2, 64, 1) == -1
+    assert L.mx_attention_workspace(4, 4, 2, 48, 1) == -1 and L.mx_attention_workspace(4, 4, 2, 64, -1) == -1
+    assert L.mx_attention_workspace(4, 4, 0, 64, 1) == -1 and L.mx_attention_workspace(4, 4, 3, 64, 1) == -1
+    assert attend(L, cache(), batch(), n=64) == -2 and "workspace" in err(L)
 
 
 def test_binding_refuses_cpu_and_wrong_types():

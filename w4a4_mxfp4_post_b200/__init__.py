@@ -118,7 +118,7 @@ def lib() -> ctypes.CDLL:
         L.norm_kq_quantize_variant.restype = ctypes.c_int
         L.kq_sf_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64]
         L.kq_sf_bytes.restype = ctypes.c_int64
-        L.mx_attention_workspace.argtypes = [ctypes.c_int64] * 4
+        L.mx_attention_workspace.argtypes = [ctypes.c_int64] * 5
         L.mx_attention_workspace.restype = ctypes.c_int64
         _lib = L
     return _lib
@@ -665,11 +665,11 @@ def mx_cache_read(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens,
     return out_k, out_v
 
 
-def mx_attention_workspace(rows: int, heads_q: int, head_dim: int, max_new: int) -> int:
+def mx_attention_workspace(rows: int, heads_q: int, heads: int, head_dim: int, max_new: int) -> int:
     """Bytes of workspace that mx_paged_attention needs for calls of these sizes."""
-    n = lib().mx_attention_workspace(int(rows), int(heads_q), int(head_dim), int(max_new))
+    n = lib().mx_attention_workspace(int(rows), int(heads_q), int(heads), int(head_dim), int(max_new))
     if n < 0:
-        raise ValueError(f"mx_attention_workspace: bad sizes {rows}, {heads_q}, {head_dim}, {max_new}")
+        raise ValueError(f"mx_attention_workspace: bad sizes {rows}, {heads_q}, {heads}, {head_dim}, {max_new}")
     return n
 
 
@@ -698,7 +698,7 @@ def mx_paged_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_
     if out is None:
         out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
     _need(out, "out", torch.bfloat16, dev, (T, hq, d))
-    need = mx_attention_workspace(T, hq, d, max_new)
+    need = mx_attention_workspace(T, hq, c.heads, d, max_new)
     if workspace is None:
         workspace = _scratch(need, dev, stream)
     _need(workspace, "workspace", torch.uint8, dev)

@@ -1639,6 +1639,7 @@ norm_kq_rows_kernel(const uint4 *__restrict__ h, const float *__restrict__ gamma
 #include "mx_cache.cuh"
 #include "mxf4_gemv.cuh"
 #include "mx_attention.cuh"
+#include "mx_chunk.cuh"
 
 // Third form of the fused normalisation + quantizer, for long rows (where the
 // per-column table and whole-row buffers of the single-pass kernel do not
@@ -2846,17 +2847,57 @@ int few_launch(const char *fn, const attn::Args &a, cudaStream_t stream)
     launch(k, unsigned(ctas), C::kWarps * 32, C::kSmem, stream, a);
     const int rc = launch_check(fn);
     if (rc != KQ_OK) return rc;
-    launch(attn::merge_kernel<C::R, C::D, 256>, unsigned(ctas), 256, 0, stream, a);
+    launch(attn::merge_kernel<C::R, C::D, 256, C::R>, unsigned(ctas), 256, 0, stream, a);
     return launch_check(fn);
 }
 
 template <int D>
+std::atomic<int> g_chunk_set[kMaxDevices];
+
+// The many-rows kernel, one CTA per SM, then the merge.
+template <int D>
+int chunk_launch(const char *fn, const attn::Args &a, cudaStream_t stream)
+{
+    using C = attn::chunk::Cfg<D>;
+    auto k = attn::chunk::chunk_kernel<C>;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    int rc = sm_count(&sms);
+    if (rc != KQ_OK) return rc;
+    if (dev < 0 || dev >= kMaxDevices || !g_chunk_set<D>[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        if (dev >= 0 && dev < kMaxDevices) g_chunk_set<D>[dev].store(1, std::memory_order_release);
+    }
+    const int ctas = sms < attn::chunk::kMaxCtas ? sms : attn::chunk::kMaxCtas;
+    launch(k, unsigned(ctas), attn::chunk::kThreads, C::kSmem, stream, a, kWaitBudget);
+    if ((rc = launch_check(fn)) != KQ_OK) return rc;
+    constexpr int kPer = attn::chunk::R / attn::chunk::kMergeRows;
+    launch(attn::merge_kernel<attn::chunk::R, D, 256, attn::chunk::kMergeRows>, unsigned(ctas * kPer), 256, 0, stream, a);
+    return launch_check(fn);
+}
+
+// Rows per kv head from which a sequence goes to the many-rows kernel.
+constexpr int64_t kChunkRows = 64;
+
+// max_new and T bound a sequence's rows; where there may be many, sequences
+// with more than kChunkRows go to the many-rows kernel (all of a single
+// sequence's) and the others to the few-rows one.
+template <int D>
 int attn_launch(const char *fn, attn::Args a, int64_t max_new, cudaStream_t stream)
 {
-    (void)max_new;
     a.rows_lo = 0;
     a.rows_hi = INT32_MAX;
-    if (max_new * a.group <= 8) return few_launch<attn::Few<D, 1>>(fn, a, stream);
+    if (max_new * a.group > kChunkRows) {
+        if (a.s.B > 1) a.rows_lo = int(kChunkRows);
+        const int rc = chunk_launch<D>(fn, a, stream);
+        if (rc != KQ_OK || a.s.B == 1) return rc;
+        a.rows_lo = 0;
+        a.rows_hi = int(kChunkRows);
+    } else if (max_new * a.group <= 8) {
+        return few_launch<attn::Few<D, 1>>(fn, a, stream);
+    }
     return few_launch<attn::Few<D, 2>>(fn, a, stream);
 }
 
@@ -3330,10 +3371,13 @@ int mx_cache_read(const mx_cache *c, const mx_batch *b, const int32_t *starts, v
     return launch_check(fn);
 }
 
-int64_t mx_attention_workspace(int64_t T, int64_t heads_q, int64_t head_dim, int64_t max_new)
+int64_t mx_attention_workspace(int64_t T, int64_t heads_q, int64_t heads, int64_t head_dim, int64_t max_new)
 {
-    if (T < 0 || heads_q < 1 || !head_dim_ok(head_dim) || max_new < 0) return -1;
-    return attn::kMaxCtas * (int64_t(sizeof(attn::Desc)) + 2 * 16 * (head_dim + 2) * 4);
+    if (T < 0 || heads < 1 || heads_q < 1 || heads_q % heads != 0 || !head_dim_ok(head_dim) || max_new < 0) return -1;
+    const int64_t most = max_new < T ? max_new : T;
+    const int64_t slots = most * (heads_q / heads) > kChunkRows ? 2 * attn::chunk::kMaxCtas * attn::chunk::R
+                                                                : 2 * attn::kMaxCtas * 16;
+    return attn::kMaxCtas * int64_t(sizeof(attn::Desc)) + slots * (head_dim + 2) * 4;
 }
 
 int mx_paged_attention(const void *q_bf16, int64_t q_stride_t, int64_t q_stride_h, const mx_cache *c,
@@ -3354,7 +3398,7 @@ int mx_paged_attention(const void *q_bf16, int64_t q_stride_t, int64_t q_stride_
     if ((rc = check_strided(fn, "q", q_bf16, q_stride_t, q_stride_h, 2)) != KQ_OK) return rc;
     if (!out_bf16) return fail(KQ_ERR_NULL, "%s: NULL pointer argument", fn);
     if (!aligned(out_bf16, 16)) return fail(KQ_ERR_ALIGN, "%s: out must be 16-byte aligned", fn);
-    const int64_t need = mx_attention_workspace(T, heads_q, c->head_dim, max_new);
+    const int64_t need = mx_attention_workspace(T, heads_q, c->heads, c->head_dim, max_new);
     if (workspace_bytes < need)
         return fail(KQ_ERR_SHAPE, "%s: workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes,
                     (long long)need);

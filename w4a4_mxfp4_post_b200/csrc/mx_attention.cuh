@@ -677,23 +677,25 @@ few_kernel(const Args a)
     }
 }
 
-// The items that were split: CTA i adds up the partials of the item that began
-// in share i's slot 2 i + 1 and went on in slots 2 (i + 1), 2 (i + 2), ...
-template <int R, int D, int THREADS>
+// The items that were split: the CTAs of share i (R / ROWS, ROWS rows each) add
+// up the partials of the item that began in its slot 2 i + 1 and went on in
+// slots 2 (i + 1), 2 (i + 2), ...
+template <int R, int D, int THREADS, int ROWS>
 __global__ void __launch_bounds__(THREADS)
 merge_kernel(const Args a)
 {
     pdl_wait();
-    const Desc d = reinterpret_cast<const Desc *>(a.work)[blockIdx.x];
+    const int share = int(blockIdx.x) / (R / ROWS), first = int(blockIdx.x) % (R / ROWS) * ROWS;
+    const Desc d = reinterpret_cast<const Desc *>(a.work)[share];
     if (d.parts == 0) return;
     const Seq q = load_seq(a, d.b);
     const int r0 = d.tile * R;
-    for (int i = threadIdx.x; i < R * D / 2; i += THREADS) {
-        const int r = i / (D / 2), ch = 2 * (i % (D / 2)), row = r0 + r;
+    for (int i = threadIdx.x; i < ROWS * D / 2; i += THREADS) {
+        const int r = first + i / (D / 2), ch = 2 * (i % (D / 2)), row = r0 + r;
         if (row >= q.rows) break;
         float mm = -INFINITY, ll = 0.0f, x = 0.0f, y = 0.0f;
         for (int k = 0; k < d.parts; ++k) {
-            const float *sl = slot<R, D>(a, k ? 2 * (int(blockIdx.x) + k) : 2 * int(blockIdx.x) + 1);
+            const float *sl = slot<R, D>(a, k ? 2 * (share + k) : 2 * share + 1);
             const float mk = sl[R * D + r], lk = sl[R * D + R + r];
             const float2 v = *reinterpret_cast<const float2 *>(sl + r * D + ch);
             const float mn = fmaxf(mm, mk);
