@@ -3,16 +3,19 @@
 // whose division of the work it shares.
 //
 // An item is 256 consecutive rows of one (sequence, kv head): two tiles of 128
-// rows.  For every unit of 128 positions the fifth-generation tensor cores
+// rows.  For every step of 128 positions the fifth-generation tensor cores
 // compute, for each tile,
 //   S = Q K^T   (128 x 128, over the channels)       into tensor memory
 //   O += P V    (128 x channels, over the positions) P from tensor memory
 // with bf16 operands and fp32 sums, P = exp2(S c - m c).
 //
-// Bound: 4 D flops per row and position on the tensor cores, and 16 exponentials
-// per clock and SM: for D = 128 both take 1024 clocks per tile and unit.  Two
-// tiles per CTA keep both busy: while one tile's softmax runs, the tensor cores
-// work for the other.
+// Bound: 4 D flops per row and position on the tensor cores and 16 exponentials
+// per clock and SM: for D = 128 both take 1024 clocks per tile and step.  Tensor
+// memory is full with S and O of two tiles (4 x 128 columns), so a tile's S
+// cannot be computed ahead, and while one tile's softmax runs the tensor cores
+// work for the other.  (S of 64 positions, twice for each tile, can be: but an
+// MMA of 128 x 64 takes as long as one of 128 x 128, about 80 clocks, and the
+// tensor cores became the limit.)
 //
 // Keys and values are decoded to bf16 once per unit and used for 256 rows.
 // code * 2^(byte - 127) is exact in bf16 for every scale byte below 253.  Of a
@@ -25,13 +28,14 @@
 //
 // Roles (16 warps):
 //   0-3, 4-7  softmax of tile 0, 1: a thread owns a row, so the maximum and the
-//             sum need no exchange.  P overwrites the upper half of S's columns.
+//             sum need no exchange.  P overwrites its S, the second 64 positions
+//             first, and P V begins with them while the first 64 are computed.
 //             O is rescaled only when a row's maximum has grown by more than 2^8
 //             since the last time (exact: P and the sum use the same stale
 //             maximum, and P <= 2^8 loses nothing in bf16).
-//   8-14      decode: a unit is 8 tasks, 32 positions of its keys or values each
+//   8-14      decode: a step is 8 tasks, 32 positions of its keys or values each
 //             (a lane per position), which the 7 warps take in turn
-//   15        issues the MMAs: P0 V, Q0 K', P1 V, Q1 K' (K' the next unit's)
+//   15        issues the MMAs: P0 V, Q0 K', P1 V, Q1 K' (K' the next step's)
 // Q, K and V lie in the 128-byte swizzle, 64 channels to a row of 128 bytes; K
 // and Q are read K-major, V with its channels as the major dimension.
 // Every wait is bounded (g_wait_timeouts).
@@ -39,28 +43,34 @@
 namespace attn {
 namespace chunk {
 
-constexpr int kTile = 128;                                   // rows of a tile, positions of a unit
+constexpr int kTile = 128;                                   // rows of a tile
+constexpr int kStep = 128;                                   // positions of a step
 constexpr int R = 2 * kTile;                                 // rows of an item
-constexpr int kThreads = 16 * 32;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kRing = 2;                                     // steps of K and of V in shared memory
 constexpr int kDecodeWarps = 7;
-constexpr int kSegs = 8;                                     // segments whose NaN positions are kept
-constexpr int kRing = 2;                                     // stages of K and of V
+constexpr int kMmaWarp = kSoftmaxWarps + kDecodeWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+// Registers a thread: 128 at launch, some moved to the softmax warpgroups.
+constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;
+static_assert(kThreads == 512 && 256 * (kSoftmaxRegs + kOtherRegs) <= 512 * 128, "the split stays within the launch's registers");
+constexpr int kSegs = 2 * kRing;                             // segments whose NaN positions are kept
 constexpr int kMergeRows = 16;                               // rows that a CTA of the merge takes
 constexpr int kMaxCtas = 192;                                // shares
 constexpr float kSlack = 8.0f;                               // log2 of how far a maximum may be stale
 constexpr uint32_t kO = 256;                                 // tensor memory: S of tile i at 128 i, O at 256 + 128 i
-static_assert(kTile == kUnit, "a unit is a tile of positions");
+static_assert(kStep == kTile && kStep == kUnit, "S is square, a step is a unit");
 
 template <int D_>
 struct Cfg {
     static constexpr int D = D_;
     static constexpr int NB = D / 32;
     static constexpr int kHalves = D > 64 ? 2 : 1;
-    static constexpr int kTileBytes = kHalves * kTile * 128; // a tile of Q, K or V
-    static constexpr int kNumBars = 4 * kRing + 10;
-    static constexpr int kSmem = (2 + 2 * kRing) * kTileBytes + 1024 + kNumBars * 8;
+    static constexpr int kQBytes = kHalves * kTile * 128;    // a tile of Q
+    static constexpr int kStepBytes = kHalves * kStep * 128; // a step of K or V
+    static constexpr int kSmem = 2 * kQBytes + 2 * kRing * kStepBytes + 1024;
     // kind::f16: fp32 sums, bf16 operands; S: N = 128, both K-major; O: N = D, B (bit 16) major in N
-    static constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kTile >> 3) << 17) | (8u << 24);
+    static constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kStep >> 3) << 17) | (8u << 24);
     static constexpr uint32_t kIdescO = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (uint32_t(D >> 3) << 17) | (8u << 24);
 };
 
@@ -101,16 +111,29 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 64 columns, waited for.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&lo)[32], float (&hi)[32])
-{
-    mma::tmem_ld32_nowait(taddr, lo);
-    mma::tmem_ld32_nowait(taddr + 32, hi);
-    tmem_wait_ld();
-}
+// Where a warp is among the segments of its CTA's share.  It lives in shared
+// memory: in registers it made the inner loops spill, and what is spilled comes
+// back from L2, for shared memory leaves the first level little room.
+struct Walk {
+    Place p;
+    Seq q;
+    int64_t left;                            // units left, this segment's among them
+    int count;                               // units of this segment
+    int t_first, t_end, steps;               // its positions and steps
+};
 
 // Whole-warp wait on a barrier; false after the budget.
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, long long budget)
@@ -119,6 +142,11 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, long long b
     if (threadIdx.x % 32 == 0) atomicAdd(&g_wait_timeouts, 1);
     return false;
 }
+
+// A value that all lanes hold, so that the compiler knows it: what the MMAs
+// take then stays in uniform registers (moving each descriptor there for every
+// MMA took more than the MMA).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
 
 // A position's codes and scale bytes of one array.
 template <int NB>
@@ -161,35 +189,49 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, uint32_t f)
                       hmul2_bf16(((v & 0x000F000Fu) * kA) & kM, f), hmul2_bf16(((v & 0x00F000F0u) * kB) & kM, f));
 }
 
-// A position into row `row` of the tile at `dst`.  NaN blocks become `nan`:
-// NaN for keys, zeros for values, whose NaN is put into the result.
+// A position into row `row` of the step at `dst`.  NaN blocks become NaN for
+// keys and zeros for values, whose NaN is put into the result.
 template <int NB>
-__device__ __forceinline__ void decode_row(const Piece<NB> &p, uint8_t *dst, int row, uint32_t nan)
+__device__ __forceinline__ void decode_row(const Piece<NB> &p, uint32_t dst, int row, bool keys)
 {
+    const uint32_t sw = (row & 7) << 4;
+    dst += row * 128;
+    auto put = [&](int ch, uint4 v) {
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (ch / 8) * (kStep * 128) + (((ch % 8) << 4) ^ sw)),
+                     "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                     : "memory");
+    };
+    uint32_t top = 0;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const uint32_t s = (p.s >> (8 * b)) & 0xffu;
-        // 2^(s - 1) as far as bf16 goes, for the scales above (rare) a second factor
-        uint32_t f = (min(s, 128u) + 126u) << 7;
-        f |= f << 16;
-        const uint32_t w[4] = {p.c[b].x, p.c[b].y, p.c[b].z, p.c[b].w};
+    for (int b = 0; b < NB; ++b) top = max(top, (p.s >> (8 * b)) & 0xffu);
+    // 2^(s - 1) as far as bf16 goes; a warp with a larger scale takes a second factor
+    const bool large = __any_sync(0xffffffffu, top > 128u);
+    if (!large) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint4 v = decode8(w[i], f);
-            if (s > 128u) {
-                uint32_t f2 = (s - 1u) << 7;
-                f2 |= f2 << 16;
-                if (s >= kNanByte) {
-                    v.x = v.y = v.z = v.w = nan;
-                } else {
-                    v.x = hmul2_bf16(v.x, f2);
-                    v.y = hmul2_bf16(v.y, f2);
-                    v.z = hmul2_bf16(v.z, f2);
-                    v.w = hmul2_bf16(v.w, f2);
-                }
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t f = (((p.s >> (8 * b)) & 0xffu) + 126u) * 0x00800080u;
+            put(4 * b, decode8(p.c[b].x, f));
+            put(4 * b + 1, decode8(p.c[b].y, f));
+            put(4 * b + 2, decode8(p.c[b].z, f));
+            put(4 * b + 3, decode8(p.c[b].w, f));
+        }
+    } else {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t s = (p.s >> (8 * b)) & 0xffu;
+            uint32_t f = (min(s, 128u) + 126u) * 0x00800080u, f2 = min(max(s, 128u) - 1u, 254u) * 0x00800080u;
+            if (s >= kNanByte) {
+                f = keys ? 0x3f803f80u : 0u;
+                f2 = keys ? 0x7fc07fc0u : 0u;
             }
-            const int ch = 4 * b + i;
-            *reinterpret_cast<uint4 *>(dst + (ch / 8) * (kTile * 128) + row * 128 + (((ch % 8) ^ (row & 7)) << 4)) = v;
+            auto twice = [&](uint32_t w) {
+                const uint4 v = decode8(w, f);
+                return make_uint4(hmul2_bf16(v.x, f2), hmul2_bf16(v.y, f2), hmul2_bf16(v.z, f2), hmul2_bf16(v.w, f2));
+            };
+            put(4 * b, twice(p.c[b].x));
+            put(4 * b + 1, twice(p.c[b].y));
+            put(4 * b + 2, twice(p.c[b].z));
+            put(4 * b + 3, twice(p.c[b].w));
         }
     }
 }
@@ -203,18 +245,16 @@ chunk_kernel(const Args a, long long budget)
     extern __shared__ __align__(16) uint8_t smem_dyn[];
     __shared__ int64_t sh[34];
     __shared__ uint32_t tmem_slot;
-    __shared__ __align__(16) uint32_t visible[4][4];   // of unit u % 4: the positions that are on a page, 32 to a word
+    __shared__ uint32_t visible[4][4];       // of step s % 4: the positions that are on a page, 32 to a word
     __shared__ int nan_first[kSegs][4];      // of segment i % kSegs, per 32 channels: the first position whose value is NaN
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
-    uint8_t *sQ = base, *sK = base + 2 * C::kTileBytes, *sV = sK + kRing * C::kTileBytes;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sV + kRing * C::kTileBytes);
-    uint64_t *kfull = bars, *kempty = bars + kRing, *vfull = bars + 2 * kRing, *vempty = bars + 3 * kRing;
-    uint64_t *qfull = bars + 4 * kRing;      // [2] Q of the tile in shared memory, the segment before put away
-    uint64_t *sfull = qfull + 2;             // [2] S ready
-    uint64_t *pfull = qfull + 4;             // [2] P ready, O in order
-    uint64_t *odone = qfull + 6;             // [2] a unit's P V done
-    uint64_t *segdone = qfull + 8;           // a segment's MMAs done
-    uint64_t *done = qfull + 9;              // all MMAs done
+    uint8_t *sQ = base, *sK = base + 2 * C::kQBytes, *sV = sK + kRing * C::kStepBytes;
+    __shared__ uint64_t kfull[kRing], kempty[kRing], vfull[kRing], vempty[kRing];
+    __shared__ uint64_t qfull[2];            // Q of the tile in shared memory, the segment before put away
+    __shared__ uint64_t sfull[2];            // S ready (and the P V before it done)
+    __shared__ uint64_t pfull[4];            // [2 tile + half] P ready, O in order
+    __shared__ uint64_t odone[2];            // the segment's last P V done
+    __shared__ uint64_t segdone, done;       // a segment's MMAs done, all MMAs done
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
     if (tid == 0) {
@@ -227,22 +267,35 @@ chunk_kernel(const Args a, long long budget)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&qfull[i], 4);
             mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i], 4);
+            mbar_init(&pfull[2 * i], 4);
+            mbar_init(&pfull[2 * i + 1], 4);
             mbar_init(&odone[i], 1);
         }
-        mbar_init(segdone, 1);
-        mbar_init(done, 1);
+        mbar_init(&segdone, 1);
+        mbar_init(&done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    Place p;
-    int64_t total, first;
-    int shares;
-    int64_t left = my_share<R, kThreads>(a, sh, p, total, first, shares);
-    Desc *dsc = reinterpret_cast<Desc *>(a.work) + blockIdx.x;
-    if (tid == 0) *dsc = Desc{0, 0, 0, 0};
-    if (left <= 0) return;
+    __shared__ Walk walks[kThreads / 32];
+    __shared__ int64_t totals[2];            // units of all shares, shares
+    {
+        Place p;
+        int64_t total, first;
+        int shares;
+        const int64_t left = my_share<R, kThreads>(a, sh, p, total, first, shares);
+        if (tid == 0) {
+            reinterpret_cast<Desc *>(a.work)[blockIdx.x] = Desc{0, 0, 0, 0};
+            totals[0] = total;
+            totals[1] = shares;
+        }
+        if (left <= 0) return;
+        if (lane == 0) {
+            walks[warp].p = p;
+            walks[warp].q = load_seq(a, p.b);
+            walks[warp].left = left;
+        }
+    }
     if (tid < kSegs * 4) nan_first[tid / 4][tid % 4] = 0x7fffffff;
-    if (warp == 15) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_slot)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -251,94 +304,120 @@ chunk_kernel(const Args a, long long budget)
     mma::tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
-    // Every role walks the same segments: units [p.unit, p.unit + count) of item (b, h, tile).
-    Seq q = load_seq(a, p.b);
+    // Every role walks the same segments: units [p.unit, p.unit + count) of item (b, h, tile), that is the
+    // positions from t_first up to t_end in `steps` steps.
+    Walk &walk = walks[warp];
     int seg = 0;                             // segments so far
-    if (warp >= 8 && warp < 15) {
+    auto segment = [&] {
+        if (lane == 0) {
+            const Place p = walk.p;
+            const Seq q = walk.q;
+            const int count = int(min(walk.left, int64_t(item_units<R>(a, q, p.tile) - p.unit)));
+            walk.count = count;
+            walk.t_first = p.unit * kUnit;
+            walk.t_end = min(row_end(a, q, min((p.tile + 1) * R, q.rows) - 1), walk.t_first + count * kUnit);
+            walk.steps = max((walk.t_end - walk.t_first + kStep - 1) / kStep, 1);
+        }
+        __syncwarp();
+    };
+    auto advance = [&] {
+        __syncwarp();
+        if (lane == 0) {
+            walk.left -= walk.count;
+            if (walk.left > 0) {
+                Place p = walk.p;
+                Seq q = walk.q;
+                next_item<R>(a, q, p);
+                walk.p = p;
+                walk.q = q;
+            }
+        }
+        __syncwarp();
+        ++seg;
+    };
+    if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
         // ---------------- keys and values into shared memory
-        int k = 0;                           // units of the segments so far
-        int turn = warp - 8;                 // this warp's next task, counted from the segment's first
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        int k = 0;                           // steps of the segments so far
+        int turn = warp - kSoftmaxWarps;                 // this warp's next task, counted from the segment's first
         bool ok = true;
-        while (left > 0 && ok) {
-            const int units = item_units<R>(a, q, p.tile), count = int(min(left, int64_t(units - p.unit)));
-            const int item_end = row_end(a, q, min((p.tile + 1) * R, q.rows) - 1);
-            const int t_first = p.unit * kUnit, t_end = min(item_end, t_first + count * kUnit);
-            const int32_t *table = a.s.table + int64_t(p.b) * a.s.table_stride;
-            // task x: unit x / 8, values if x & 4, positions 32 (x & 3) + lane
-            auto row_of = [&](int64_t x) -> int64_t {
-                if (x >= int64_t(count) * 8) return -1;
-                const int t = t_first + int(x >> 3) * kUnit + 32 * int(x & 3) + lane;
-                if (t >= t_end) return -1;
-                const int64_t r = strip_row(a, table, p.h, t & ~15);
-                return r < 0 ? -1 : r + (t & 15);
+        while (walk.left > 0 && ok) {
+            segment();
+            const int32_t *table = a.s.table + int64_t(walk.p.b) * a.s.table_stride;
+            const int t_first = walk.t_first, t_end = walk.t_end, steps = walk.steps, head = walk.p.h;
+            const int tasks = steps * 8;
+            // task x: step x / 8, values if x & 4, positions 32 (x & 3) + lane.  The pages are looked up one task
+            // ahead of the codes, the codes one task ahead of their use.
+            auto page_index = [&](int t) { return a.page_shift >= 0 ? t >> a.page_shift : t / a.s.page; };
+            auto position = [&](int x) { return t_first + (x >> 3) * kStep + 32 * (x & 3) + lane; };
+            auto page_of = [&](int x) -> int {
+                const int64_t t = int64_t(t_first) + int64_t(x >> 3) * kStep + 32 * (x & 3) + lane;
+                return t < t_end ? __ldg(table + page_index(int(t))) : -1;
             };
-            auto load = [&](Piece<NB> &x, int64_t task, int64_t row) {
-                const bool is_v = task & 4;
-                load_piece<NB>(x, is_v ? a.vc : a.kc, is_v ? a.vs : a.ks, row);
+            auto load = [&](Piece<NB> &v, int x, int page) {
+                const int t = position(x);
+                const bool is_v = x & 4;
+                int64_t row = -1;
+                if (page >= 0 && page < a.s.num_pages)
+                    row = (int64_t(page) * a.s.heads + head) * a.s.page + (t - page_index(t) * a.s.page);
+                load_piece<NB>(v, is_v ? a.vc : a.kc, is_v ? a.vs : a.ks, row);
             };
             Piece<NB> next;
-            load(next, turn, row_of(turn));
-            int64_t ahead = row_of(turn + kDecodeWarps);
-            int64_t x = turn;
-            for (; x < int64_t(count) * 8; x += kDecodeWarps) {
+            load(next, turn, page_of(turn));
+            int ahead = page_of(turn + kDecodeWarps);
+            int x = turn;
+            for (; x < tasks; x += kDecodeWarps) {
                 const Piece<NB> cur = next;
                 load(next, x + kDecodeWarps, ahead);
-                ahead = row_of(x + 2 * kDecodeWarps);
-                const int u = int(x >> 3), part = int(x & 3), ku = k + u, st = ku % kRing, row = 32 * part + lane;
+                ahead = page_of(x + 2 * kDecodeWarps);
+                const int u = x >> 3, part = x & 3, ku = k + u, st = ku % kRing, row = 32 * part + lane;
                 const bool is_v = x & 4;
                 if (ku >= kRing && !wait(is_v ? &vempty[st] : &kempty[st], ((ku / kRing) - 1) & 1, budget)) {
                     ok = false;
                     break;
                 }
                 if (is_v) {
-                    bool nan = false;
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) nan |= ((cur.s >> (8 * b)) & 0xffu) >= kNanByte;
-                    if (nan) {
-#pragma unroll
-                        for (int b = 0; b < NB; ++b)
-                            if (((cur.s >> (8 * b)) & 0xffu) >= kNanByte)
-                                atomicMin(&nan_first[seg % kSegs][b], t_first + u * kUnit + row);
-                    }
+                    for (int b = 0; b < NB; ++b)
+                        if (((cur.s >> (8 * b)) & 0xffu) >= kNanByte)
+                            atomicMin(&nan_first[seg % kSegs][b], t_first + u * kStep + row);
                 } else {
                     const uint32_t on = __ballot_sync(0xffffffffu, cur.on);
                     if (lane == 0) visible[ku & 3][part] = on;
                 }
-                decode_row<NB>(cur, (is_v ? sV : sK) + st * C::kTileBytes, row, is_v ? 0u : 0x7fc07fc0u);
+                decode_row<NB>(cur, smem_addr(is_v ? sV : sK) + st * C::kStepBytes, row, !is_v);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(is_v ? &vfull[st] : &kfull[st]);
             }
-            turn = int(x - int64_t(count) * 8);
-            k += count;
-            left -= count;
-            ++seg;
-            if (left > 0) next_item<R>(a, q, p);
+            turn = x - tasks;
+            k += steps;
+            advance();
         }
-    } else if (warp == 15) {
+    } else if (warp == kMmaWarp) {
         // ---------------- the MMAs
-        int k = 0, n0 = 0, n1 = 0;           // units, units of each tile so far
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        int k = 0, n1 = 0;                   // steps, steps of the second tile so far
         bool ok = true;
-        const uint32_t aQ = smem_addr(sQ), aK = smem_addr(sK), aV = smem_addr(sV);
+        const uint32_t tm = uniform(tmem), aQ = uniform(smem_addr(sQ));
+        const uint32_t aK = aQ + 2 * C::kQBytes, aV = aK + kRing * C::kStepBytes;
         auto qk = [&](int i, int st) {
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                const uint32_t off = (j / 4) * (kTile * 128) + (j % 4) * 32;
-                umma_ss(tmem + i * 128, desc(aQ + i * C::kTileBytes + off, 16), desc(aK + st * C::kTileBytes + off, 16),
-                        C::kIdescS, j > 0);
-            }
+            for (int j = 0; j < D / 16; ++j)
+                umma_ss(tm + i * 128, desc(aQ + i * C::kQBytes + (j / 4) * (kTile * 128) + (j % 4) * 32, 16),
+                        desc(aK + st * C::kStepBytes + (j / 4) * (kStep * 128) + (j % 4) * 32, 16), C::kIdescS, j > 0);
             gemm::umma_commit_w(&sfull[i]);
         };
-        auto pv = [&](int i, int st, bool add) {
+        auto pv = [&](int i, int st, int half, bool add) {
 #pragma unroll
-            for (int j = 0; j < kTile / 16; ++j)
-                umma_ts(tmem + kO + i * 128, tmem + i * 128 + 64 + j * 8,
-                        desc(aV + st * C::kTileBytes + j * 16 * 128, kTile * 128), C::kIdescO, add || j > 0);
-            gemm::umma_commit_w(&odone[i]);
+            for (int j = 4 * half; j < 4 * half + 4; ++j)    // P: 32 columns in either half of S
+                umma_ts(tm + kO + i * 128, tm + i * 128 + half * 64 + (j % 4) * 8,
+                        desc(aV + st * C::kStepBytes + j * 16 * 128, kStep * 128), C::kIdescO, add || j > 4 * half);
         };
-        while (left > 0 && ok) {
-            const int units = item_units<R>(a, q, p.tile), count = int(min(left, int64_t(units - p.unit)));
-            const bool two = q.rows - p.tile * R > kTile;
+        while (uniform(walk.left > 0) && ok) {
+            segment();
+            const int n = int(uniform(uint32_t(walk.steps)));
+            const bool two = uniform(walk.q.rows - walk.p.tile * R > kTile);
             if (!wait(&kfull[k % kRing], (k / kRing) & 1, budget) || !wait(&qfull[0], seg & 1, budget) ||
                 !wait(&qfull[1], seg & 1, budget))
                 break;
@@ -346,75 +425,86 @@ chunk_kernel(const Args a, long long budget)
             qk(0, k % kRing);
             if (two) qk(1, k % kRing);
             gemm::umma_commit_w(&kempty[k % kRing]);
-            for (int u = 0; u < count; ++u, ++k) {
+            for (int u = 0; u < n && ok; ++u, ++k) {
                 const int st = k % kRing, sn = (k + 1) % kRing;
-                const bool more = u + 1 < count;
-                if (!wait(&vfull[st], (k / kRing) & 1, budget) || !wait(&pfull[0], n0 & 1, budget)) {
-                    ok = false;
-                    break;
-                }
-                ++n0;
+                const bool more = u + 1 < n;
+                ok = wait(&vfull[st], (k / kRing) & 1, budget) && wait(&pfull[1], k & 1, budget);
+                if (!ok) break;
                 mma::tc_fence_after();
-                pv(0, st, u > 0);
+                pv(0, st, 1, u > 0);
+                ok = wait(&pfull[0], k & 1, budget);
+                if (!ok) break;
+                mma::tc_fence_after();
+                pv(0, st, 0, true);
                 if (!two) gemm::umma_commit_w(&vempty[st]);
                 if (more) {
-                    if (!wait(&kfull[sn], ((k + 1) / kRing) & 1, budget)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = wait(&kfull[sn], ((k + 1) / kRing) & 1, budget);
+                    if (!ok) break;
                     mma::tc_fence_after();
                     qk(0, sn);
+                } else {
+                    gemm::umma_commit_w(&odone[0]);
                 }
                 if (two) {
-                    if (!wait(&pfull[1], n1 & 1, budget)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = wait(&pfull[3], n1 & 1, budget);
+                    if (!ok) break;
+                    mma::tc_fence_after();
+                    pv(1, st, 1, u > 0);
+                    ok = wait(&pfull[2], n1 & 1, budget);
+                    if (!ok) break;
                     ++n1;
                     mma::tc_fence_after();
-                    pv(1, st, u > 0);
+                    pv(1, st, 0, true);
                     gemm::umma_commit_w(&vempty[st]);
                     if (more) qk(1, sn);
+                    else gemm::umma_commit_w(&odone[1]);
                 }
                 if (more) gemm::umma_commit_w(&kempty[sn]);
             }
             if (!ok) break;
-            gemm::umma_commit_w(segdone);
-            ++seg;
-            left -= count;
-            if (left > 0) next_item<R>(a, q, p);
+            gemm::umma_commit_w(&segdone);
+            advance();
         }
         // every MMA issued has completed before the tensor memory is freed
-        gemm::umma_commit_w(done);
-        wait(done, 0, budget);
+        gemm::umma_commit_w(&done);
+        wait(&done, 0, budget);
     } else {
         // ---------------- softmax: thread = row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int i = warp / 4, row = tid % kTile;
         const uint32_t lanes = uint32_t(warp % 4) << 21;                     // 32 (warp % 4) in the lane field
-        const uint32_t tS = tmem + lanes + i * 128, tP = tS + 64, tO = tmem + lanes + kO + i * 128;
-        int n = 0;                           // units of this tile so far
-        int k = 0;                           // units so far
+        const uint32_t tS = tmem + lanes + i * 128, tO = tmem + lanes + kO + i * 128;
+        int n = 0;                           // steps of this tile so far
+        int k = 0;                           // steps so far
+        int mine_segs = 0;                   // segments of this tile so far
         const float c = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);
         bool ok = true;
-        while (left > 0 && ok) {
-            const int units = item_units<R>(a, q, p.tile), count = int(min(left, int64_t(units - p.unit)));
-            const int r0 = p.tile * R + i * kTile, r = r0 + row;
-            // Nobody writes this segment's slot yet, and whoever read it (five segments ago) is through: the next
-            // segment's first MMA waits for both tiles' softmax.
-            if (tid < 4) nan_first[(seg + 3) % kSegs][tid] = 0x7fffffff;
-            if (r0 >= q.rows) {
+        while (walk.left > 0 && ok) {
+            segment();
+            const int steps = walk.steps;
+            const int r0 = walk.p.tile * R + i * kTile;
+            // The values run kRing steps, so at most kRing segments ahead: nobody writes this slot before this
+            // segment's P V, and who read it (kRing segments ago) is through, since a segment's first MMA waits
+            // for both tiles' softmax.
+            if (tid < 4) nan_first[(seg + kRing) % kSegs][tid] = 0x7fffffff;
+            if (r0 >= walk.q.rows) {
                 // nothing to do, but the next segment begins after both tiles' last, and this tile's arrivals must
                 // not run ahead of the segments
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&qfull[i]);
-                if (!wait(segdone, seg & 1, budget)) break;
+                if (!wait(&segdone, seg & 1, budget)) break;
             } else {
-                const bool mine = r < q.rows;
-                const int token = r / a.group, head = p.h * a.group + r - token * a.group;
-                // Q: rows of the tile, channels of 8 in the decoders' order; the sign (or zero) of the scale goes into it
+                // positions from the step's first that the row sees; one that is not there sees all, for nothing
+                int lim;
+                // Q: rows of the tile, channels of 8 in the decoders' order; the sign (or zero) of the scale
+                // goes into it
                 {
+                    const Seq q = walk.q;
+                    const int r = r0 + row, token = r / a.group, head = walk.p.h * a.group + r - token * a.group;
+                    const bool mine = r < q.rows;
+                    lim = mine ? row_end(a, q, r) - walk.t_first : 0x7fffffff;
                     const __nv_bfloat16 *src = a.q + int64_t(q.lo + token) * a.q_st + int64_t(head) * a.q_sh;
-                    uint8_t *dst = sQ + i * C::kTileBytes + row * 128;
+                    uint8_t *dst = sQ + i * C::kQBytes + row * 128;
                     const uint32_t sgn = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
                     for (int ch = 0; ch < D / 8; ++ch) {
@@ -434,56 +524,48 @@ chunk_kernel(const Args a, long long budget)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&qfull[i]);
                 }
-                const int lim = mine ? row_end(a, q, r) : 0x7fffffff;        // a row that is not there sees all, for nothing
-                float m = -INFINITY, l = 0.0f;                               // m: of S, as used
-                for (int u = 0; u < count; ++u, ++n) {
+                int lim_min = __reduce_min_sync(0xffffffffu, lim);     // of the warp's rows
+                float m = -INFINITY, l = 0.0f;                               // the maximum in use, the sum
+                for (int u = 0; u < steps; ++u, ++n, lim -= kStep, lim_min -= kStep) {
                     if (!wait(&sfull[i], n & 1, budget)) {
                         ok = false;
                         break;
                     }
                     mma::tc_fence_after();
-                    const int t0 = (p.unit + u) * kUnit;
-                    uint32_t vis[4];
-                    bool masked = lim < t0 + kUnit;
-                    {
-                        const uint4 on = *reinterpret_cast<const uint4 *>(visible[(k + u) & 3]);
-                        vis[0] = on.x, vis[1] = on.y, vis[2] = on.z, vis[3] = on.w;
-                        masked |= (on.x & on.y & on.z & on.w) != 0xffffffffu;
-                    }
-                    masked = __any_sync(0xffffffffu, masked);
-                    if (masked) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int see = lim - t0 - 32 * j;
-                            vis[j] &= see >= 32 ? 0xffffffffu : see <= 0 ? 0u : (1u << see) - 1u;
-                        }
-                    }
-                    auto mask = [&](float (&v)[32], uint32_t bits) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = (bits >> e) & 1 ? v[e] : -INFINITY;
-                    };
+                    const uint32_t *on = visible[(k + u) & 3];
                     float x[32], y[32];
+                    if (lim_min < kStep || (on[0] & on[1] & on[2] & on[3]) != 0xffffffffu) {
+                        // rare: what the rows do not see becomes -infinity in tensor memory
+#pragma unroll 1
+                        for (int j = 0; j < 4; ++j) {
+                            const int see = lim - 32 * j;
+                            const uint32_t bits = on[j] & (see >= 32 ? 0xffffffffu : see <= 0 ? 0u : (1u << see) - 1u);
+                            mma::tmem_ld32_nowait(tS + 32 * j, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t w[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    w[e] = (bits >> (16 * h + e)) & 1 ? __float_as_uint(x[16 * h + e]) : 0xff800000u;
+                                tmem_st16(tS + 32 * j + 16 * h, w);
+                            }
+                        }
+                        tmem_wait_st();
+                    }
                     float top = m, top2 = -INFINITY;
-                    tmem_ld64(tS, x, y);
-                    if (masked) {
-                        mask(x, vis[0]);
-                        mask(y, vis[1]);
-                    }
+                    auto maximum = [&](uint32_t src) {
+                        mma::tmem_ld32_nowait(src, x);
+                        mma::tmem_ld32_nowait(src + 32, y);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        top = fmaxf(top, x[e]);
-                        top2 = fmaxf(top2, y[e]);
-                    }
-                    tmem_ld64(tS + 64, x, y);
-                    if (masked) {
-                        mask(x, vis[2]);
-                        mask(y, vis[3]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        top = fmaxf(top, x[e]);
-                        top2 = fmaxf(top2, y[e]);
-                    }
+                        for (int e = 0; e < 32; e += 2) {
+                            top = fmaxf(fmaxf(top, x[e]), x[e + 1]);
+                            top2 = fmaxf(fmaxf(top2, y[e]), y[e + 1]);
+                        }
+                    };
+                    maximum(tS);
+                    maximum(tS + 64);
                     top = fmaxf(top, top2);
                     const bool grown = top != m && (top - m) * c > kSlack;
                     if (__any_sync(0xffffffffu, grown)) {
@@ -491,23 +573,15 @@ chunk_kernel(const Args a, long long budget)
                         if (grown) m = top;
                         l *= al;
                         if (u > 0) {
-                            if (!wait(&odone[i], (n - 1) & 1, budget)) {
-                                ok = false;
-                                break;
-                            }
-                            mma::tc_fence_after();
 #pragma unroll 1
-                            for (int j = 0; j < NB; ++j) {
-                                float o[32];
-                                mma::tmem_ld32_nowait(tO + 32 * j, o);
+                            for (int j = 0; j < 2 * NB; ++j) {
+                                float o[16];
+                                tmem_ld16(tO + 16 * j, o);
                                 tmem_wait_ld();
+                                uint32_t w[16];
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    uint32_t w[16];
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[16 * h + e] * al);
-                                    tmem_st16(tO + 32 * j + 16 * h, w);
-                                }
+                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * al);
+                                tmem_st16(tO + 16 * j, w);
                             }
                         }
                     }
@@ -528,80 +602,90 @@ chunk_kernel(const Args a, long long budget)
                         }
                         tmem_st16(dst, w);
                     };
-                    probs(x, tP + 32);
-                    probs(y, tP + 48);
-                    tmem_ld64(tS, x, y);
-                    if (masked) {
-                        mask(x, vis[0]);
-                        mask(y, vis[1]);
-                    }
-                    probs(x, tP);
-                    probs(y, tP + 16);
+                    auto ready = [&](int half) {
+                        tmem_wait_st();
+                        mma::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&pfull[2 * i + half]);
+                    };
+                    probs(x, tS + 64);
+                    probs(y, tS + 80);
+                    ready(1);
+                    mma::tmem_ld32_nowait(tS, x);
+                    mma::tmem_ld32_nowait(tS + 32, y);
+                    tmem_wait_ld();
+                    probs(x, tS);
+                    probs(y, tS + 16);
                     l = (sum0.x + sum0.y) + (sum1.x + sum1.y);
-                    tmem_wait_st();
-                    mma::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&pfull[i]);
+                    ready(0);
                 }
-                if (!ok || !wait(&odone[i], (n - 1) & 1, budget)) {
+                if (!ok || !wait(&odone[i], mine_segs++ & 1, budget)) {
                     ok = false;
                     break;
                 }
                 mma::tc_fence_after();
-                const bool whole = count == units;
+                const Seq q = walk.q;
+                const Place p = walk.p;
+                const int r = p.tile * R + i * kTile + row;
+                const bool mine = r < q.rows;
+                const int sees = mine ? row_end(a, q, r) : 0;
+                const int units = item_units<R>(a, q, p.tile);
+                const bool whole = walk.count == units;
                 float *sl = slot<R, D>(a, 2 * int(blockIdx.x) + (p.unit == 0 ? 1 : 0));
                 const int ir = i * kTile + row;                              // row of the item
+                const int token = r / a.group, head = p.h * a.group + r - token * a.group;
                 const float inv = 1.0f / l;
                 if (!whole && mine) {
                     sl[R * D + ir] = m == -INFINITY ? m : m * c;
                     sl[R * D + R + ir] = l;
                 }
 #pragma unroll 1
-                for (int j = 0; j < NB; ++j) {
-                    float o[32];
-                    mma::tmem_ld32_nowait(tO + 32 * j, o);
+                for (int j = 0; j < 2 * NB; ++j) {
+                    float o[16];
+                    tmem_ld16(tO + 16 * j, o);
                     tmem_wait_ld();
-                    const bool nan = nan_first[seg % kSegs][j] < lim;
-                    if (mine)
+                    const bool nan = nan_first[seg % kSegs][j / 2] < sees;
+                    if (mine) {
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        // columns hold channels 0 4 1 5 2 6 3 7
-                        float v[8] = {o[8 * g], o[8 * g + 2], o[8 * g + 4], o[8 * g + 6],
-                                      o[8 * g + 1], o[8 * g + 3], o[8 * g + 5], o[8 * g + 7]};
+                        for (int h = 0; h < 2; ++h) {
+                            // columns hold channels 0 4 1 5 2 6 3 7
+                            float v[8] = {o[8 * h], o[8 * h + 2], o[8 * h + 4], o[8 * h + 6],
+                                          o[8 * h + 1], o[8 * h + 3], o[8 * h + 5], o[8 * h + 7]};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            if (nan) v[e] = __uint_as_float(0x7fc00000u);
-                            if (whole) v[e] = l == 0.0f && v[e] == 0.0f ? 0.0f : v[e] * inv;
-                        }
-                        if (whole) {
-                            *reinterpret_cast<uint4 *>(a.out + (int64_t(q.lo + token) * a.hq + head) * D + 32 * j + 8 * g) =
-                                make_uint4(mma::pack_bf16x2(v[0], v[1]), mma::pack_bf16x2(v[2], v[3]),
-                                           mma::pack_bf16x2(v[4], v[5]), mma::pack_bf16x2(v[6], v[7]));
-                        } else {
-                            float *dst = sl + int64_t(ir) * D + 32 * j + 8 * g;
-                            *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-                            *reinterpret_cast<float4 *>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                            for (int e = 0; e < 8; ++e) {
+                                if (nan) v[e] = __uint_as_float(0x7fc00000u);
+                                if (whole) v[e] = l == 0.0f && v[e] == 0.0f ? 0.0f : v[e] * inv;
+                            }
+                            const int ch = 16 * j + 8 * h;
+                            if (whole) {
+                                *reinterpret_cast<uint4 *>(a.out + (int64_t(q.lo + token) * a.hq + head) * D + ch) =
+                                    make_uint4(mma::pack_bf16x2(v[0], v[1]), mma::pack_bf16x2(v[2], v[3]),
+                                               mma::pack_bf16x2(v[4], v[5]), mma::pack_bf16x2(v[6], v[7]));
+                            } else {
+                                float *dst = sl + int64_t(ir) * D + ch;
+                                *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+                                *reinterpret_cast<float4 *>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                            }
                         }
                     }
                 }
                 mma::tc_fence_before();
                 if (tid == 0 && !whole && p.unit == 0) {
-                    const int64_t last = total * (blockIdx.x + 1) / shares - left + units - 1;
+                    const int64_t total = totals[0], shares = totals[1];
+                    const int64_t end = total * (blockIdx.x + 1) / shares - walk.left + units - 1;
                     int64_t e = blockIdx.x + 1;
-                    while (total * (e + 1) / shares <= last) ++e;
-                    *dsc = Desc{p.b, p.h, p.tile, int(e - blockIdx.x + 1)};
+                    while (total * (e + 1) / shares <= end) ++e;
+                    reinterpret_cast<Desc *>(a.work)[blockIdx.x] = Desc{p.b, p.h, p.tile, int(e - blockIdx.x + 1)};
                 }
             }
-            k += count;
-            left -= count;
-            ++seg;
-            if (left > 0) next_item<R>(a, q, p);
+            k += steps;
+            advance();
         }
     }
 
     mma::tc_fence_before();
     __syncthreads();
-    if (warp == 15) {
+    if (warp == kMmaWarp) {
         mma::tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
