@@ -79,7 +79,11 @@ def attention(q, cache, table, cu, lens, scale, causal):
     each p_j is then off by the factor 1 + 2 e + 2^-21 (the exponential's own
     error), and half a bf16 step for the second product (2^-8); sums of up to
     L terms in fp32 add (L + 8) 2^-23; a numerator and a denominator; and
-    half a bf16 step of the result.
+    half a bf16 step of the result.  Where the second product takes p in fp16,
+    as p 2^15 times the position's scale relative to the largest, a term below
+    fp16's normal numbers is off by half of its smallest step, 2^-25, times a
+    code of at most 6: L 2^-40 * 6 * 2^(largest scale) in all, over a sum of
+    probabilities that is at least 1 (the maximum's own).
     """
     kc, ks, vc, vs = cache
     T, hq, d = q.shape
@@ -121,7 +125,10 @@ def attention(q, cache, table, cu, lens, scale, causal):
                     e = abs(scale) * ((d + 2) * 2.0 ** -23 * qk + 2.0 ** -40 * qq.abs().amax(-1) * ka) + 4 * FP32 * top
                 else:
                     e = torch.zeros(hi - lo, dtype=torch.float64, device=q.device)
+                vtop = vs[table[b][(torch.arange(n, device=q.device) // kc.shape[2]).clamp(max=table.shape[1] - 1)].long().clamp(0, kc.shape[0] - 1), h,
+                          torch.arange(n, device=q.device) % kc.shape[2]] if n and table.shape[1] else vs[:0, h, 0]
+                vtop = torch.where((vtop < 253) & on[:, None], vtop, torch.zeros_like(vtop)).amax().item() if vtop.numel() else 0
                 rel = 2 * (2 * e + 2.0 ** -21 + (n + 8) * 2.0 ** -23) + BF16
-                tt = rel[:, None] * S * (1 + BF16) + BF16 * y.abs()
+                tt = (rel[:, None] * S + n * 2.0 ** -40 * 6 * 2.0 ** (vtop - 127)) * (1 + BF16) + BF16 * y.abs()
                 tol[lo:hi, j] = torch.where(hit, torch.zeros_like(tt), tt)
     return out, tol

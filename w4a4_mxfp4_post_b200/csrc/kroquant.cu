@@ -2847,7 +2847,7 @@ int few_launch(const char *fn, const attn::Args &a, cudaStream_t stream)
     launch(k, unsigned(ctas), C::kWarps * 32, C::kSmem, stream, a);
     const int rc = launch_check(fn);
     if (rc != KQ_OK) return rc;
-    launch(attn::merge_kernel<C::R, C::D, 256, C::R>, unsigned(ctas), 256, 0, stream, a);
+    launch(attn::merge_kernel<C::R, C::D, 256, C::kMergeRows>, unsigned(ctas * (C::R / C::kMergeRows)), 256, 0, stream, a);
     return launch_check(fn);
 }
 

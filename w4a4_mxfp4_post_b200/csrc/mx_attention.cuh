@@ -25,6 +25,7 @@ namespace attn {
 
 constexpr int kUnit = 128;                   // positions per unit of work
 constexpr int kMaxCtas = 512;                // shares (the workspace has two slots for each)
+constexpr int kWindow = 12;                  // binades of value scales that fp16 products take together
 constexpr uint32_t kNanByte = 253;           // K and V scale bytes from here up read as NaN
 
 struct Args {
@@ -160,6 +161,12 @@ __device__ __forceinline__ int64_t my_share(const Args &a, int64_t *sh, Place &p
     return last - first;
 }
 
+// The share that unit u is in: the last i with total * i / shares <= u.
+__device__ __forceinline__ int64_t share_of(int64_t u, int64_t total, int64_t shares)
+{
+    return ((u + 1) * shares + total - 1) / total - 1;
+}
+
 // The next item after (b, h, tile): tiles, then heads, then sequences that have rows.
 template <int R>
 __device__ __forceinline__ void next_item(const Args &a, Seq &q, Place &p)
@@ -215,10 +222,16 @@ __device__ __forceinline__ float pow2(int e)
 // power of two per row that puts its largest element in [2^15, 2^16): exact
 // down to 2^-32 of it, else off by at most 2^-40 of it.
 // The values' scale varies along the summed dimension, so it has to be in an
-// operand: values are expanded to bf16 by shifts (the code's bits 8, 7, 6 and
-// 15 are code * 2^-126, which one packed multiply by 2^(126 + scale) makes
-// exact: fp32's range in 8 bits), relative to the warp's running largest value
-// scale, with P in bf16: half a step, 2^-8 of each probability.
+// operand.  It goes into P, which is small: 2 multiplies per 32 channels and 16
+// positions instead of one per pair of values.  Values are then plain fp16 codes
+// (ldmatrix.trans brings 4 codes of two positions into a register, 6 bit
+// operations pair up 16 codes, cvt unpacks them), and a 32-block of channels has
+// its own P' = p 2^15 2^(scale - top) in fp16, top the warp's largest value scale
+// so far: half a step, 2^-11 of each probability, or 2^-40 of the largest
+// probability times the largest scale, whichever is more.  Stages where a scale
+// lies more than 2^12 below top (rare) take bf16 instead, values expanded by
+// shifts (the code's bits 8, 7, 6 and 15 are code * 2^-126, which one packed
+// multiply by 2^(126 + scale - top) makes exact) and P in bf16.
 // P^T leaves the first product with positions along the rows and enters the
 // second along the columns: movmatrix transposes it.
 //
@@ -231,16 +244,15 @@ struct Few {
     static constexpr int D = D_, NT = NT_;
     static constexpr int R = 8 * NT;
     static constexpr int kWarps = 4;
+    static constexpr int kMergeRows = 2;                     // rows that a CTA of the merge takes
     static constexpr int kStages = 3;
     static constexpr int NB = D / 32;
-    static constexpr int DP = D <= 64 ? 64 : 128;            // channels of the V tile (D = 32, 96: the rest is not stored)
-    static constexpr int MT = DP / 16;
-    static constexpr int kKRow = D >= 96 ? 64 : D / 2;       // bytes of a key's row in the stage
-    static constexpr int kVRow = DP / 2;
-    static constexpr int kKBytes = 32 * kKRow, kVBytes = 32 * kVRow;
+    static constexpr int MT = 2 * NB;                        // 16-channel tiles of O
+    static constexpr int kRow = D >= 96 ? 64 : D / 2;        // bytes of a position's codes in the stage
+    static constexpr int kBytes = 32 * kRow;                 // of keys or values
     static constexpr int kScaleBytes = 32 * NB;              // of keys; the values' follow
-    static constexpr int kStage = kKBytes + kVBytes + 2 * kScaleBytes;
-    static constexpr int kTable = 32 * 4 * 4 + 16 * 4 * 4;   // key scales (fp32), value scales (bf16 pairs)
+    static constexpr int kStage = 2 * kBytes + 2 * kScaleBytes;
+    static constexpr int kTable = 32 * 4 * 4 + 16 * 4 * 4;   // key scales (fp32), value scales (16-bit pairs)
     static constexpr int kWarpBytes = kStages * kStage + kTable;
     static constexpr int kOutRow = D + 4;                    // floats
     static constexpr int kMerge = kWarps * R * (kOutRow + 2) * 4;
@@ -269,6 +281,23 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x)
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2_f16(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Four 8 x 8 matrices of 16-bit elements, transposed: with rows of 16 bytes of
+// codes, register i holds codes 4 g .. 4 g + 3 of positions 2 c and 2 c + 1.
+__device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
 }
 
 // Code p (0..3) of both 16-bit halves as bf16 values code * 2^-126: sign to bit
@@ -306,7 +335,16 @@ few_kernel(const Args a)
     float *ktab = reinterpret_cast<float *>(ring + ST * C::kStage);          // [32 positions][4]
     uint32_t *vtab = reinterpret_cast<uint32_t *>(ktab + 128);               // [16 pairs][4]
     const uint32_t ring_s = smem_addr(ring);
-    const int vblk = C::DP == 128 ? g >> 1 : g >> 2;         // the 32 channels that this thread's V rows are in
+    // ldmatrix: this lane's row of the strip (matrices: positions 0-7, 8-15 of two 32-blocks) and its swizzle
+    const int vrow = lane & 15, vsw = D >= 96 ? (vrow >> 1) & 3 : D == 64 ? (vrow >> 2) & 1 : 0, vsel = lane >> 4;
+
+    // Where piece i of a strip (chunk i % NB of row i / NB) goes: chunks xor-swizzled by row.  For NB a power of two
+    // 32 pieces are 32 / NB rows, a multiple of 8, so the next ones have the same swizzle.
+    auto place = [](int i) {
+        const int r = i / NB, ch = i % NB;
+        return r * C::kRow + (D >= 96 ? ch ^ ((r >> 1) & 3) : D == 64 ? ch ^ ((r >> 2) & 1) : ch) * 16;
+    };
+    const uint32_t place0 = place(lane);
 
     Seq q = load_seq(a, p.b);
     while (left > 0) {
@@ -377,41 +415,40 @@ few_kernel(const Args a)
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
         }
-        int vtop = 0;                                        // the largest value scale byte so far
+        int vtop = 0, kref = 0;                              // the largest value and key scale bytes so far
+        float cs[NT][2];                                     // what brings S to units of log 2
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) cs[t][i] = a.scale_log2 * pow2(max(qe[t][i] - 127, -126));
         uint32_t on_page = 0;                                // two bits per stage in flight: its strips have a page
 
         const int t_first = p.unit * kUnit + warp * 32;
         auto fetch = [&](int t0, int slot_i) {               // stage: positions t0 .. t0 + 31
             uint32_t bits = 0;
             if (t0 < t_end) {
-                int64_t row[2];
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    row[s] = t0 + 16 * s < t_end ? strip_row(a, table, p.h, t0 + 16 * s) : -1;
-                    bits |= row[s] >= 0 ? 1u << s : 0u;
-                }
                 const uint32_t dst = ring_s + slot_i * C::kStage;
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    const int idx = lane + 32 * j, s = idx / (16 * NB), in = idx - s * 16 * NB;
-                    const int r = in / NB, ch = in % NB;
-                    const int64_t rw = s ? row[1] : row[0];
-                    const uint32_t size = rw >= 0 ? 16 : 0;
-                    const int64_t off = (rw >= 0 ? rw : 0) * (D / 2) + in * 16;
-                    const int kch = D >= 96 ? ch ^ ((r >> 1) & 3) : D == 64 ? ch ^ ((r >> 2) & 1) : ch;
-                    gemv::cp_async16_sized(dst + (16 * s + r) * C::kKRow + kch * 16, size ? a.kc + off : a.kc, size);
-                    const int vs = (r & 8) | ((r & 1) << 2) | ((r >> 1) & 3);
-                    const int vch = C::DP == 128 ? ch ^ (vs & 2) : ch;
-                    gemv::cp_async16_sized(dst + C::kKBytes + (16 * s + vs) * C::kVRow + vch * 16, size ? a.vc + off : a.vc,
-                                           size);
-                }
-                if (lane < 4 * NB) {                         // scales: 16 NB bytes of a strip are contiguous
-                    const int s = (lane / NB) & 1, piece = lane % NB;
-                    const bool is_v = lane >= 2 * NB;
-                    const int64_t rw = s ? row[1] : row[0];
-                    const uint8_t *base = is_v ? a.vs : a.ks;
-                    gemv::cp_async16_sized(dst + C::kKBytes + C::kVBytes + lane * 16,
-                                           rw >= 0 ? base + rw * NB + piece * 16 : base, rw >= 0 ? 16 : 0);
+                for (int s = 0; s < 2; ++s) {                // strips of 16 positions, contiguous in the pool
+                    const int64_t row = t0 + 16 * s < t_end ? strip_row(a, table, p.h, t0 + 16 * s) : -1;
+                    const uint32_t size = row >= 0 ? 16 : 0;
+                    bits |= row >= 0 ? 1u << s : 0u;
+                    const int64_t at = row >= 0 ? row : 0;
+                    const uint8_t *k = a.kc + at * (D / 2) + lane * 16, *v = a.vc + at * (D / 2) + lane * 16;
+#pragma unroll
+                    for (int j = 0; j < (NB + 1) / 2; ++j) { // 16 NB pieces, 32 at a time
+                        if (NB % 2 == 0 || 32 * j + lane < 16 * NB) {
+                            const uint32_t to = dst + 16 * s * C::kRow + (NB == 3 ? place(lane + 32 * j) : place0 + 32 / NB * j * C::kRow);
+                            gemv::cp_async16_sized(to, k + 512 * j, size);
+                            gemv::cp_async16_sized(to + C::kBytes, v + 512 * j, size);
+                        }
+                    }
+                    if (lane < 2 * NB) {                     // scales: 16 NB bytes of a strip are contiguous
+                        const bool is_v = lane >= NB;
+                        const int piece = is_v ? lane - NB : lane;
+                        gemv::cp_async16_sized(dst + 2 * C::kBytes + (is_v ? C::kScaleBytes : 0) + s * 16 * NB + piece * 16,
+                                               (is_v ? a.vs : a.ks) + at * NB + piece * 16, size);
+                    }
                 }
             }
             gemv::cp_commit();
@@ -435,46 +472,80 @@ few_kernel(const Args a)
             // ---- scales of the stage: lane = position
             const bool valid = t0 + lane < t_end && ((pages >> (lane >> 4)) & 1);
             const uint32_t mask = __ballot_sync(0xffffffffu, valid);
-            int kb[NB], vb[NB], ktop = 0, vmax = 0;
+            int kb[NB], vb[NB], ktop = 0, vmax = 0, vmin = 255;
             bool vnan = false;
             {
-                const uint8_t *ks = st + C::kKBytes + C::kVBytes + lane * NB;
+                const uint8_t *ks = st + 2 * C::kBytes + lane * NB;
+                if constexpr (NB == 4) {
+                    const uint32_t wk = *reinterpret_cast<const uint32_t *>(ks);
+                    const uint32_t wv = *reinterpret_cast<const uint32_t *>(ks + C::kScaleBytes);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        kb[b] = (wk >> (8 * b)) & 0xff;
+                        vb[b] = (wv >> (8 * b)) & 0xff;
+                    }
+                } else {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        kb[b] = ks[b];
+                        vb[b] = ks[C::kScaleBytes + b];
+                    }
+                }
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    kb[b] = ks[b];
-                    vb[b] = valid ? ks[C::kScaleBytes + b] : 0;
-                    if (kb[b] < int(kNanByte)) ktop = max(ktop, valid ? kb[b] : 0);
+                    if (kb[b] < int(kNanByte)) ktop = max(ktop, kb[b]);
                     if (vb[b] >= int(kNanByte)) vnan = true;
-                    else vmax = max(vmax, vb[b]);
+                    else if (vb[b] > 0) {
+                        vmax = max(vmax, vb[b]);
+                        vmin = min(vmin, vb[b]);
+                    }
+                }
+                if (!valid) {
+                    ktop = vmax = 0;
+                    vmin = 255;
+                    vnan = false;
                 }
             }
-            if (__any_sync(0xffffffffu, vnan)) {             // rare: values that are NaN count as zero here
+            if (__any_sync(0xffffffffu, vnan || vmax > vtop || ktop > kref)) {
+                // rare but for the first stages: values that are NaN, which count as zero here, and larger scales
+                if (vnan) {
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    if (vb[b] >= int(kNanByte)) {
-                        atomicMin(&nan_first[b], t0 + lane);
-                        vb[b] = -1;
-                    }
+                    for (int b = 0; b < NB; ++b)
+                        if (vb[b] >= int(kNanByte)) {
+                            atomicMin(&nan_first[b], t0 + lane);
+                            vb[b] = -512;
+                        }
+                }
+                ktop = __reduce_max_sync(0xffffffffu, ktop);
+                if (ktop > kref) {
+                    kref = ktop;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) cs[t][i] = a.scale_log2 * pow2(max(min(qe[t][i] + kref - 127, 127), -126));
+                }
+                vmax = __reduce_max_sync(0xffffffffu, vmax);
+                if (vmax > vtop) {
+                    const float f = pow2(vtop - vmax);
+                    vtop = vmax;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[t][i][e] *= f;
+                }
             }
-            ktop = __reduce_max_sync(0xffffffffu, ktop);
-            vmax = __reduce_max_sync(0xffffffffu, vmax);
-            if (vmax > vtop) {
-                const float f = pow2(vtop - vmax);
-                vtop = vmax;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[t][i][e] *= f;
-            }
+            const bool wide = __any_sync(0xffffffffu, vmin < vtop - kWindow);
             {
                 float kv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    kv[b] = kb[b] >= int(kNanByte) ? __uint_as_float(0x7fc00000u) : pow2(kb[b] - ktop);
-                    // bf16 2^(126 + byte - vtop): at most 2^126, zero for a position that counts for nothing
-                    const uint32_t f = valid && vb[b] >= 0 ? uint32_t(max(vb[b] - vtop + 253, 0)) << 7 : 0u;
+                    const int ke = max(kb[b] - kref + 127, 0);
+                    kv[b] = __uint_as_float(kb[b] >= int(kNanByte) ? 0x7fc00000u : uint32_t(ke) << 23);
+                    // fp16 2^(byte - vtop) or bf16 2^(126 + byte - vtop), zero for a position that counts for nothing
+                    const int e = valid ? vb[b] - vtop : -512;
+                    const uint32_t f = wide ? uint32_t(max(e + 253, 0)) << 7 : uint32_t(max(e + 15, 0)) << 10;
                     reinterpret_cast<uint16_t *>(vtab)[((lane >> 1) * 4 + b) * 2 + (lane & 1)] = uint16_t(f);
                 }
                 *reinterpret_cast<float4 *>(ktab + 4 * lane) = make_float4(kv[0], kv[1], kv[2], kv[3]);
@@ -493,10 +564,10 @@ few_kernel(const Args a)
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     const int ch = D >= 96 ? b ^ ((g >> 1) & 3) : D == 64 ? b ^ ((g >> 2) & 1) : b;
-                    const uint8_t *kr = st + (16 * sp + g) * C::kKRow + ch * 16 + 4 * c;
+                    const uint8_t *kr = st + (16 * sp + g) * C::kRow + ch * 16 + 4 * c;
                     uint32_t x[4], y[4];
                     gemv::codes_f16(*reinterpret_cast<const uint32_t *>(kr), x);
-                    gemv::codes_f16(*reinterpret_cast<const uint32_t *>(kr + 8 * C::kKRow), y);
+                    gemv::codes_f16(*reinterpret_cast<const uint32_t *>(kr + 8 * C::kRow), y);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -512,38 +583,33 @@ few_kernel(const Args a)
 
             // ---- softmax: scores in units of log 2, the running maximum of each column
             const bool masked = mask != 0xffffffffu || t0 + 32 > lim_min;
-            uint32_t pt[2][NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int sp = 0; sp < 2; ++sp)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[sp][t][i] *= cs[t][i & 1];
+                if (masked) {
+#pragma unroll
+                    for (int sp = 0; sp < 2; ++sp)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = 16 * sp + 8 * (i >> 1) + g;
+                            if (!((mask >> row) & 1) || t0 + row >= lim[t][i & 1]) s[sp][t][i] = -INFINITY;
+                        }
+                }
                 float mx[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float cs = a.scale_log2 * pow2(max(min(qe[t][i] + ktop - 127, 127), -126));
-#pragma unroll
-                    for (int sp = 0; sp < 2; ++sp) {
-                        s[sp][t][i] *= cs;
-                        s[sp][t][2 + i] *= cs;
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int sp = 0; sp < 2; ++sp)
-#pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) {
-                                const int row = 16 * sp + 8 * hf + g;
-                                if (!((mask >> row) & 1) || t0 + row >= lim[t][i]) s[sp][t][2 * hf + i] = -INFINITY;
-                            }
-                    }
-                    float v = fmaxf(fmaxf(s[0][t][i], s[0][t][2 + i]), fmaxf(s[1][t][i], s[1][t][2 + i]));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    mx[i] = fmaxf(m[t][i], v);
-                }
+                for (int i = 0; i < 2; ++i) mx[i] = fmaxf(fmaxf(s[0][t][i], s[0][t][2 + i]), fmaxf(s[1][t][i], s[1][t][2 + i]));
                 if (__any_sync(0xffffffffu, mx[0] > m[t][0] || mx[1] > m[t][1])) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float al = mx[i] > m[t][i] ? ex2(m[t][i] - mx[i]) : 1.0f;
-                        m[t][i] = mx[i];
+                        float v = mx[i];
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                        const float al = v > m[t][i] ? ex2(m[t][i] - v) : 1.0f;
+                        m[t][i] = fmaxf(m[t][i], v);
                         l[t][i] *= al;
 #pragma unroll
                         for (int k = 0; k < MT; ++k) {
@@ -553,54 +619,88 @@ few_kernel(const Args a)
                     }
                 }
                 // a column that has seen nothing has maximum -infinity: its probabilities are zeros
-                const float mu[2] = {m[t][0] == -INFINITY ? 0.0f : m[t][0], m[t][1] == -INFINITY ? 0.0f : m[t][1]};
+                // (2^15 of each: the sum has the factor, too)
+                const float mu[2] = {m[t][0] == -INFINITY ? 0.0f : m[t][0] - 15.0f, m[t][1] == -INFINITY ? 0.0f : m[t][1] - 15.0f};
 #pragma unroll
-                for (int sp = 0; sp < 2; ++sp) {
-                    float e[4];
+                for (int sp = 0; sp < 2; ++sp)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        e[i] = ex2(s[sp][t][i] - mu[i & 1]);
-                        l[t][i & 1] += e[i];
+                        s[sp][t][i] = ex2(s[sp][t][i] - mu[i & 1]);
+                        l[t][i & 1] += s[sp][t][i];
                     }
-                    pt[sp][t][0] = movmatrix(mma::pack_bf16x2(e[0], e[1]));
-                    pt[sp][t][1] = movmatrix(mma::pack_bf16x2(e[2], e[3]));
-                }
             }
 
-            // ---- O^T: positions 2 c, + 1 and + 8, + 9 of a strip; channels DP / 8 * g ..
+            // ---- O^T: positions 2 c, + 1 and + 8, + 9 of a strip; channels 32 b + 4 g ..
+            const uint32_t vst = ring_s + (it % ST) * C::kStage + C::kBytes + vrow * C::kRow;
+            // registers: block b2's positions 2 c and 2 c + 8, then block b2 + 1's
+            auto codes = [&](uint32_t (&r)[4], int sp, int b2) {
+                ldmatrix_trans(r, vst + 16 * sp * C::kRow + ((min(b2 + vsel, NB - 1) ^ vsw) << 4));
+            };
+            auto factors = [&](uint32_t (&f)[4], int pair) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(vtab + pair * 4);
+                f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+            };
+            if (!wide) {
 #pragma unroll
-            for (int sp = 0; sp < 2; ++sp) {
-                const uint32_t fa = vtab[(8 * sp + c) * 4 + vblk], fb = vtab[(8 * sp + 4 + c) * 4 + vblk];
-                const uint8_t *vr = st + C::kKBytes + (16 * sp + c) * C::kVRow;
-                constexpr int WPT = C::DP / 64;              // words of a position per thread
-                uint32_t w[4][WPT];                          // positions 2 c, 2 c + 1, 2 c + 8, 2 c + 9: slots c, + 4, + 8, + 12
+                for (int sp = 0; sp < 2; ++sp) {
+                    uint32_t f0[4], f1[4], pt[NT][2];
+                    factors(f0, 8 * sp + c);
+                    factors(f1, 8 * sp + 4 + c);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if constexpr (C::DP == 128) {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(vr + 4 * k * C::kVRow + (((g >> 1) ^ (c & 2)) << 4) +
-                                                                         (g & 1) * 8);
-                        w[k][0] = v.x;
-                        w[k][1] = v.y;
-                    } else {
-                        w[k][0] = *reinterpret_cast<const uint32_t *>(vr + 4 * k * C::kVRow + 4 * g);
+                    for (int t = 0; t < NT; ++t) {
+                        pt[t][0] = movmatrix(gemv::pack_f16x2(s[sp][t][0], s[sp][t][1]));
+                        pt[t][1] = movmatrix(gemv::pack_f16x2(s[sp][t][2], s[sp][t][3]));
                     }
-                }
 #pragma unroll
-                for (int x = 0; x < WPT; ++x)
+                    for (int b2 = 0; b2 < NB; b2 += 2) {
+                        uint32_t r[4];
+                        codes(r, sp, b2);
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {         // four codes of both positions
-                        const uint32_t sel = hf ? 0x7632 : 0x5410;
-                        const uint32_t u = __byte_perm(w[0][x], w[1][x], sel), v = __byte_perm(w[2][x], w[3][x], sel);
-                        const uint32_t a0 = hmul2_bf16(code_bf16<0>(u), fa), a1 = hmul2_bf16(code_bf16<1>(u), fa);
-                        const uint32_t a2 = hmul2_bf16(code_bf16<2>(u), fa), a3 = hmul2_bf16(code_bf16<3>(u), fa);
-                        const uint32_t b0 = hmul2_bf16(code_bf16<0>(v), fb), b1 = hmul2_bf16(code_bf16<1>(v), fb);
-                        const uint32_t b2 = hmul2_bf16(code_bf16<2>(v), fb), b3 = hmul2_bf16(code_bf16<3>(v), fb);
+                        for (int b = b2; b < b2 + 2 && b < NB; ++b) {
+                            const uint32_t x = r[2 * (b - b2)], y = r[2 * (b - b2) + 1];
+                            const uint32_t u = __byte_perm(x, y, 0x5410), v = __byte_perm(x, y, 0x7632);
+                            uint32_t ev[4], od[4];           // codes 0, 2 (1, 3) of 2 c, + 1, then of 2 c + 8, + 9
+                            gemv::codes_f16((u & 0x0F0F0F0Fu) | ((v << 4) & 0xF0F0F0F0u), ev);
+                            gemv::codes_f16(((u >> 4) & 0x0F0F0F0Fu) | (v & 0xF0F0F0F0u), od);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            mma_bf16(o[t][4 * x + 2 * hf], a0, a1, b0, b1, pt[sp][t][0], pt[sp][t][1]);
-                            mma_bf16(o[t][4 * x + 2 * hf + 1], a2, a3, b2, b3, pt[sp][t][0], pt[sp][t][1]);
+                            for (int t = 0; t < NT; ++t) {
+                                const uint32_t p0 = hmul2_f16(pt[t][0], f0[b]), p1 = hmul2_f16(pt[t][1], f1[b]);
+                                gemv::mma_f16(o[t][2 * b], ev[0], od[0], ev[2], od[2], p0, p1);
+                                gemv::mma_f16(o[t][2 * b + 1], ev[1], od[1], ev[3], od[3], p0, p1);
+                            }
                         }
                     }
+                }
+            } else {
+#pragma unroll
+                for (int sp = 0; sp < 2; ++sp) {
+                    uint32_t f0[4], f1[4], pt[NT][2];
+                    factors(f0, 8 * sp + c);
+                    factors(f1, 8 * sp + 4 + c);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        pt[t][0] = movmatrix(mma::pack_bf16x2(s[sp][t][0], s[sp][t][1]));
+                        pt[t][1] = movmatrix(mma::pack_bf16x2(s[sp][t][2], s[sp][t][3]));
+                    }
+#pragma unroll
+                    for (int b2 = 0; b2 < NB; b2 += 2) {
+                        uint32_t r[4];
+                        codes(r, sp, b2);
+#pragma unroll
+                        for (int b = b2; b < b2 + 2 && b < NB; ++b) {
+                            const uint32_t x = r[2 * (b - b2)], y = r[2 * (b - b2) + 1];
+                            const uint32_t x0 = hmul2_bf16(code_bf16<0>(x), f0[b]), x1 = hmul2_bf16(code_bf16<1>(x), f0[b]);
+                            const uint32_t x2 = hmul2_bf16(code_bf16<2>(x), f0[b]), x3 = hmul2_bf16(code_bf16<3>(x), f0[b]);
+                            const uint32_t y0 = hmul2_bf16(code_bf16<0>(y), f1[b]), y1 = hmul2_bf16(code_bf16<1>(y), f1[b]);
+                            const uint32_t y2 = hmul2_bf16(code_bf16<2>(y), f1[b]), y3 = hmul2_bf16(code_bf16<3>(y), f1[b]);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                mma_bf16(o[t][2 * b], x0, x1, y0, y1, pt[t][0], pt[t][1]);
+                                mma_bf16(o[t][2 * b + 1], x2, x3, y2, y3, pt[t][0], pt[t][1]);
+                            }
+                        }
+                    }
+                }
             }
         }
         gemv::cp_wait<0>();
@@ -622,11 +722,11 @@ few_kernel(const Args a)
                     mw[warp * R + r] = m[t][i];
                     lw[warp * R + r] = v;
                 }
-                float *dst = ow + (warp * R + r) * C::kOutRow + g * (C::DP / 8);
+                float *dst = ow + (warp * R + r) * C::kOutRow + 4 * g;
 #pragma unroll
-                for (int k = 0; k < MT; ++k)
-                    if (g * (C::DP / 8) + 2 * k < D)
-                        *reinterpret_cast<float2 *>(dst + 2 * k) = make_float2(o[t][k][i] * vs, o[t][k][2 + i] * vs);
+                for (int b = 0; b < NB; ++b)
+                    *reinterpret_cast<float4 *>(dst + 32 * b) =
+                        make_float4(o[t][2 * b][i] * vs, o[t][2 * b][2 + i] * vs, o[t][2 * b + 1][i] * vs, o[t][2 * b + 1][2 + i] * vs);
             }
         __syncthreads();
         const bool whole = count == units;
@@ -666,9 +766,7 @@ few_kernel(const Args a)
         if (!whole && p.unit == 0 && threadIdx.x == 0) {
             // the item starts here and goes on: the shares up to the one with its last unit hold it
             const int64_t last = at_unit + units - 1;
-            int64_t k = blockIdx.x + 1;
-            while (total * (k + 1) / shares <= last) ++k;
-            *desc = Desc{p.b, p.h, p.tile, int(k - blockIdx.x + 1)};
+            *desc = Desc{p.b, p.h, p.tile, int(share_of(last, total, shares)) - int(blockIdx.x) + 1};
         }
         __syncthreads();
         at_unit += count;
@@ -685,31 +783,72 @@ __global__ void __launch_bounds__(THREADS)
 merge_kernel(const Args a)
 {
     pdl_wait();
+    __shared__ float weight[ROWS][kMaxCtas];                 // of each part
+    __shared__ float sums[ROWS];
     const int share = int(blockIdx.x) / (R / ROWS), first = int(blockIdx.x) % (R / ROWS) * ROWS;
     const Desc d = reinterpret_cast<const Desc *>(a.work)[share];
     if (d.parts == 0) return;
     const Seq q = load_seq(a, d.b);
-    const int r0 = d.tile * R;
-    for (int i = threadIdx.x; i < ROWS * D / 2; i += THREADS) {
-        const int r = first + i / (D / 2), ch = 2 * (i % (D / 2)), row = r0 + r;
-        if (row >= q.rows) break;
-        float mm = -INFINITY, ll = 0.0f, x = 0.0f, y = 0.0f;
-        for (int k = 0; k < d.parts; ++k) {
-            const float *sl = slot<R, D>(a, k ? 2 * (share + k) : 2 * share + 1);
-            const float mk = sl[R * D + r], lk = sl[R * D + R + r];
-            const float2 v = *reinterpret_cast<const float2 *>(sl + r * D + ch);
-            const float mn = fmaxf(mm, mk);
-            const float f0 = mm == -INFINITY ? 0.0f : ex2(mm - mn);
-            const float f1 = mk == -INFINITY ? (lk == 0.0f ? 0.0f : lk) : ex2(mk - mn);
-            // (0 * NaN: what an earlier part made NaN stays so)
-            x = fmaf(v.x, f1, mm == -INFINITY && x == x ? 0.0f : x * f0);
-            y = fmaf(v.y, f1, mm == -INFINITY && y == y ? 0.0f : y * f0);
-            ll = fmaf(lk, f1, mm == -INFINITY && ll == ll ? 0.0f : ll * f0);
-            mm = mn;
+    const int r0 = d.tile * R + first, rows = min(ROWS, q.rows - r0);
+    auto part = [&](int k) { return slot<R, D>(a, k ? 2 * (share + k) : 2 * share + 1); };
+    // a warp per row: the maximum, then every part's weight and the sum, lanes over the parts
+    for (int r = threadIdx.x / 32; r < rows; r += THREADS / 32) {
+        const int lane = threadIdx.x % 32;
+        float mm = -INFINITY;
+        for (int k = lane; k < d.parts; k += 32) {
+            const float mk = part(k)[R * D + first + r];
+            weight[r][k] = mk;
+            mm = fmaxf(mm, mk);
         }
-        const float inv = 1.0f / ll;
-        const uint32_t v = ll == 0.0f && x == 0.0f ? 0u : mma::pack_bf16x2(x * inv, y * inv);
-        *reinterpret_cast<uint32_t *>(a.out + (int64_t(q.lo + row / a.group) * a.hq + d.h * a.group + row % a.group) * D + ch) = v;
+#pragma unroll
+        for (int i = 16; i; i >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, i));
+        float ll = 0.0f;
+        for (int k = lane; k < d.parts; k += 32) {
+            const float mk = weight[r][k], lk = part(k)[R * D + R + first + r];
+            // a part that saw nothing has nothing; a NaN sum reaches the result
+            const float f = mk == -INFINITY ? (lk == 0.0f ? 0.0f : lk) : ex2(mk - mm);
+            weight[r][k] = f;
+            ll = fmaf(lk, f, ll);
+        }
+#pragma unroll
+        for (int i = 16; i; i >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, i);
+        if (lane == 0) sums[r] = ll;
+    }
+    __syncthreads();
+    // four channels of a row per thread, the parts dealt out to G groups of threads
+    constexpr int E = ROWS * D / 4, G = THREADS / E;
+    static_assert(G >= 1, "a thread for every four channels");
+    __shared__ float4 some[G][E];
+    const int e = threadIdx.x % E, grp = threadIdx.x / E, r = e / (D / 4), ch = 4 * (e % (D / 4));
+    if (grp < G && r < rows) {
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int k = grp; k < d.parts; k += G) {
+            const float4 v = *reinterpret_cast<const float4 *>(part(k) + (first + r) * D + ch);
+            const float f = weight[r][k];
+            x.x = fmaf(v.x, f, x.x);
+            x.y = fmaf(v.y, f, x.y);
+            x.z = fmaf(v.z, f, x.z);
+            x.w = fmaf(v.w, f, x.w);
+        }
+        some[grp][e] = x;
+    }
+    __syncthreads();
+    if (threadIdx.x < E && r < rows) {
+        float4 x = some[0][e];
+#pragma unroll
+        for (int i = 1; i < G; ++i) {
+            const float4 v = some[i][e];
+            x.x += v.x;
+            x.y += v.y;
+            x.z += v.z;
+            x.w += v.w;
+        }
+        const int row = r0 + r;
+        const float ll = sums[r], inv = 1.0f / ll;
+        const uint2 v = ll == 0.0f && x.x == 0.0f ? make_uint2(0u, 0u)
+                                                  : make_uint2(mma::pack_bf16x2(x.x * inv, x.y * inv), mma::pack_bf16x2(x.z * inv, x.w * inv));
+        *reinterpret_cast<uint2 *>(a.out + (int64_t(q.lo + row / a.group) * a.hq + d.h * a.group + row % a.group) * D + ch) = v;
     }
 }
 

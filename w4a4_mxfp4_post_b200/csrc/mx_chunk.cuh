@@ -55,7 +55,7 @@ constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;
 static_assert(kThreads == 512 && 256 * (kSoftmaxRegs + kOtherRegs) <= 512 * 128, "the split stays within the launch's registers");
 constexpr int kSegs = 2 * kRing;                             // segments whose NaN positions are kept
-constexpr int kMergeRows = 16;                               // rows that a CTA of the merge takes
+constexpr int kMergeRows = 8;                                // rows that a CTA of the merge takes
 constexpr int kMaxCtas = 192;                                // shares
 constexpr float kSlack = 8.0f;                               // log2 of how far a maximum may be stale
 constexpr uint32_t kO = 256;                                 // tensor memory: S of tile i at 128 i, O at 256 + 128 i
@@ -673,9 +673,8 @@ chunk_kernel(const Args a, long long budget)
                 if (tid == 0 && !whole && p.unit == 0) {
                     const int64_t total = totals[0], shares = totals[1];
                     const int64_t end = total * (blockIdx.x + 1) / shares - walk.left + units - 1;
-                    int64_t e = blockIdx.x + 1;
-                    while (total * (e + 1) / shares <= end) ++e;
-                    reinterpret_cast<Desc *>(a.work)[blockIdx.x] = Desc{p.b, p.h, p.tile, int(e - blockIdx.x + 1)};
+                    reinterpret_cast<Desc *>(a.work)[blockIdx.x] =
+                        Desc{p.b, p.h, p.tile, int(share_of(end, total, shares)) - int(blockIdx.x) + 1};
                 }
             }
             k += steps;
