@@ -146,10 +146,16 @@ def _call(name: str, device, *args) -> None:
         raise KroQuantError(name, rc, kq_last_error())
 
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream, device):
@@ -157,20 +163,27 @@ def _stream(stream, device):
     torch stream must belong to `device`."""
     torch = _torch()
     if stream is None:
+        raw = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
+        if raw is not None and device is not None and device.index is not None:
+            return ctypes.c_void_p(raw(device.index))        # without making a Stream object
         stream = torch.cuda.current_stream(device)
     elif isinstance(stream, torch.cuda.Stream) and device is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def _ptr(t) -> ctypes.c_void_p:
-    return ctypes.c_void_p(t.data_ptr() if t is not None and t.numel() > 0 else 0)
+def _ptr(t) -> int:
+    return t.data_ptr() if t is not None and t.numel() > 0 else 0
 
 
 def _need(t, name, dtype, device=None, shape=None):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    # what calls give almost always, in as few steps as it takes
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (device is None or t.device == device) and \
+            (shape is None or t.shape == shape):
+        return t
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:

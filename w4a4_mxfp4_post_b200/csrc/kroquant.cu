@@ -1961,7 +1961,8 @@ enum KernelId {
     kKqDirect, kKqDirectF32, kKqPacked, kKqPackedF32, kSqPacked, kMxPacked, kFold,
     kKqStaged, kSqStaged, kMxStaged, kKqMma, kKqMmaF32, kKqLu, kFwht, kInverse, kDequant, kNormKq,
     kKqPackedSf, kMxF32, kMxF32Sf, kSfRelayout, kNormRows, kNormKqSf, kKqRing,
-    kCacheWrite, kCacheWriteF32, kCacheRead, kCacheReadF32, kNumKernels
+    kCacheWrite, kCacheWriteF32, kCacheRead, kCacheReadF32,
+    kNumKernels = kCacheWrite + 16               // (the four for each head dimension)
 };
 std::atomic<int> g_ctas_per_sm[kNumKernels][kMaxDevices];
 
@@ -2738,6 +2739,45 @@ int check_strided(const char *fn, const char *what, const void *p, int64_t st, i
     return KQ_OK;
 }
 
+// --- the cache's reads and writes: a warp per token and array, as many CTAs as
+// the device holds at once ---
+template <typename K>
+int cache_grid(int kernel_id, K kern, int T, unsigned *grid)
+{
+    int64_t threads = 0;
+    const int rc = resident_threads(KernelId(kernel_id), reinterpret_cast<const void *>(kern), &threads);
+    if (rc != KQ_OK) return rc;
+    const int64_t need = 2 * int64_t(T) * 32;
+    *grid = unsigned(((threads < need ? threads : need) + kThreads - 1) / kThreads);
+    return KQ_OK;
+}
+
+template <int NB>
+int cache_write(const char *fn, const void *k, int64_t kst, int64_t ksh, const void *v, int64_t vst, int64_t vsh,
+                bool f32, const mx_cache *c, const cache::Seqs &s, cudaStream_t stream)
+{
+    auto kern = f32 ? cache::write_kernel<true, NB> : cache::write_kernel<false, NB>;
+    unsigned grid = 0;
+    const int rc = cache_grid((f32 ? kCacheWriteF32 : kCacheWrite) + 4 * (NB - 1), kern, s.T, &grid);
+    if (rc != KQ_OK) return rc;
+    launch(kern, grid, kThreads, 0, stream, k, v, kst, ksh, vst, vsh, reinterpret_cast<uint32_t *>(c->k_codes),
+           c->k_scales, reinterpret_cast<uint32_t *>(c->v_codes), c->v_scales, s);
+    return launch_check(fn);
+}
+
+template <int NB>
+int cache_read(const char *fn, const mx_cache *c, const int32_t *starts, void *out_k, void *out_v, bool f32,
+               const cache::Seqs &s, cudaStream_t stream)
+{
+    auto kern = f32 ? cache::read_kernel<true, NB> : cache::read_kernel<false, NB>;
+    unsigned grid = 0;
+    const int rc = cache_grid((f32 ? kCacheReadF32 : kCacheRead) + 4 * (NB - 1), kern, s.T, &grid);
+    if (rc != KQ_OK) return rc;
+    launch(kern, grid, kThreads, 0, stream, reinterpret_cast<const uint32_t *>(c->k_codes), c->k_scales,
+           reinterpret_cast<const uint32_t *>(c->v_codes), c->v_scales, starts, out_k, out_v, s);
+    return launch_check(fn);
+}
+
 // --- the few-row product ---
 struct GemvArgs {
     const __nv_bfloat16 *x;
@@ -3331,18 +3371,12 @@ int mx_cache_write(const void *k, int64_t k_stride_t, int64_t k_stride_h, const 
     if ((rc = check_seq_pointers(fn, c, b, true)) != KQ_OK) return rc;
     if ((rc = check_strided(fn, "k", k, k_stride_t, k_stride_h, elem)) != KQ_OK) return rc;
     if ((rc = check_strided(fn, "v", v, v_stride_t, v_stride_h, elem)) != KQ_OK) return rc;
-    const int nb = int(c->head_dim / kBlk);
-    const int64_t total = T * 2 * c->heads * nb;
-    auto kern = in_f32 ? cache::write_kernel<true> : cache::write_kernel<false>;
-    int64_t target = 0;
-    if ((rc = resident_threads(in_f32 ? kCacheWriteF32 : kCacheWrite, reinterpret_cast<const void *>(kern), &target)) !=
-        KQ_OK)
-        return rc;
-    const int64_t n = target < total ? target : total;
-    launch(kern, unsigned((n + kThreads - 1) / kThreads), kThreads, 0, stream, k, v, k_stride_t, k_stride_h,
-           v_stride_t, v_stride_h, reinterpret_cast<uint4 *>(c->k_codes), c->k_scales,
-           reinterpret_cast<uint4 *>(c->v_codes), c->v_scales, s, nb);
-    return launch_check(fn);
+    switch (c->head_dim / kBlk) {
+    case 1: return cache_write<1>(fn, k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, in_f32 != 0, c, s, stream);
+    case 2: return cache_write<2>(fn, k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, in_f32 != 0, c, s, stream);
+    case 3: return cache_write<3>(fn, k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, in_f32 != 0, c, s, stream);
+    default: return cache_write<4>(fn, k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, in_f32 != 0, c, s, stream);
+    }
 }
 
 int mx_cache_read(const mx_cache *c, const mx_batch *b, const int32_t *starts, void *out_k, void *out_v, int out_f32,
@@ -3357,18 +3391,12 @@ int mx_cache_read(const mx_cache *c, const mx_batch *b, const int32_t *starts, v
     if (!out_k || !out_v) return fail(KQ_ERR_NULL, "%s: NULL pointer argument", fn);
     if (!aligned(out_k, 16) || !aligned(out_v, 16) || !aligned(starts, 4))
         return fail(KQ_ERR_ALIGN, "%s: out_k and out_v must be 16-byte aligned, starts 4-byte aligned", fn);
-    const int nb = int(c->head_dim / kBlk);
-    const int64_t total = T * 2 * c->heads * nb;
-    auto kern = out_f32 ? cache::read_kernel<true> : cache::read_kernel<false>;
-    int64_t target = 0;
-    if ((rc = resident_threads(out_f32 ? kCacheReadF32 : kCacheRead, reinterpret_cast<const void *>(kern), &target)) !=
-        KQ_OK)
-        return rc;
-    const int64_t n = target < total ? target : total;
-    launch(kern, unsigned((n + kThreads - 1) / kThreads), kThreads, 0, stream,
-           reinterpret_cast<const uint4 *>(c->k_codes), c->k_scales, reinterpret_cast<const uint4 *>(c->v_codes),
-           c->v_scales, starts, out_k, out_v, s, nb);
-    return launch_check(fn);
+    switch (c->head_dim / kBlk) {
+    case 1: return cache_read<1>(fn, c, starts, out_k, out_v, out_f32 != 0, s, stream);
+    case 2: return cache_read<2>(fn, c, starts, out_k, out_v, out_f32 != 0, s, stream);
+    case 3: return cache_read<3>(fn, c, starts, out_k, out_v, out_f32 != 0, s, stream);
+    default: return cache_read<4>(fn, c, starts, out_k, out_v, out_f32 != 0, s, stream);
+    }
 }
 
 int64_t mx_attention_workspace(int64_t T, int64_t heads_q, int64_t heads, int64_t head_dim, int64_t max_new)

@@ -63,108 +63,150 @@ __device__ __forceinline__ int64_t cache_row(const Seqs &s, int b, int h, int64_
     return (int64_t(p) * s.heads + h) * s.page + (pos - int64_t(j) * s.page);
 }
 
-// Quantize the keys and values of new tokens into the cache.  One thread per
-// 32-block: it reads 64 (128) bytes of its row, quantizes them as the other
-// MXFP4 kernels do and writes 16 bytes of codes and the scale byte.  Bound by
+// Both kernels: a warp per token and array, a lane per 8 channels (a block of 32
+// is 4 neighbouring lanes), so that every access of a warp is contiguous but for
+// the heads' distance in the pool, and what finds the token's place is done once
+// for heads x D channels.  Up to kPieces loads of a lane are in flight.  Bound by
 // the bytes read and written.
-template <bool F32>
+constexpr int kPieces = 4;
+
+// Place of row t: its sequence's pool row for head 0 (-1 if on no page), or no
+// sequence (false).  Position: the last new tokens' (len) or from `starts`.
+__device__ __forceinline__ bool row_place(const Seqs &s, int t, const int32_t *starts, bool read, int64_t &row)
+{
+    const int b = seq_of_row(s, t);
+    if (b < 0) return false;
+    int lo, hi;
+    seq_rows(s, b, lo, hi);
+    const int64_t pos = read ? int64_t(t - lo) + (starts ? __ldg(starts + b) : 0) : int64_t(__ldg(s.len + b)) - hi + t;
+    row = cache_row(s, b, 0, pos);
+    return true;
+}
+
+// Quantize the keys and values of new tokens into the cache, as the other MXFP4
+// kernels do: the four lanes of a block share its largest magnitude (bits order
+// like magnitudes, and what is not finite is above all that is).
+template <bool F32, int NB>
 __global__ void __launch_bounds__(kThreads)
 write_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t kst, int64_t ksh, int64_t vst,
-             int64_t vsh, uint4 *__restrict__ kc, uint8_t *__restrict__ ks, uint4 *__restrict__ vc,
-             uint8_t *__restrict__ vs, Seqs s, int nb)
+             int64_t vsh, uint32_t *__restrict__ kc, uint8_t *__restrict__ ks, uint32_t *__restrict__ vc,
+             uint8_t *__restrict__ vs, Seqs s)
 {
     pdl_wait();
-    const int per_row = s.heads * nb;
-    const int64_t total = int64_t(s.T) * 2 * per_row;
-    const int64_t stride = int64_t(gridDim.x) * kThreads;
-    for (int64_t g = int64_t(blockIdx.x) * kThreads + threadIdx.x; g < total; g += stride) {
-        const int t = int(g / (2 * per_row));
-        int r = int(g - int64_t(t) * (2 * per_row));
-        const bool is_v = r >= per_row;
-        if (is_v) r -= per_row;
-        const int h = r / nb, j = r - h * nb;
-        const int b = seq_of_row(s, t);
-        if (b < 0) continue;
-        int lo, hi;
-        seq_rows(s, b, lo, hi);
-        const int64_t row = cache_row(s, b, h, int64_t(__ldg(s.len + b)) - hi + t);
-        if (row < 0) continue;
-        const int64_t off = int64_t(t) * (is_v ? vst : kst) + int64_t(h) * (is_v ? vsh : ksh) + 32 * j;
-        float x[32];
-        if constexpr (F32) {
-            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(is_v ? v : k) + off);
+    constexpr int PH = 4 * NB;                               // pieces of a head
+    const int lane = threadIdx.x % 32, pieces = s.heads * PH;
+    const int64_t warps = int64_t(gridDim.x) * (kThreads / 32);
+    for (int64_t task = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; task < 2 * int64_t(s.T); task += warps) {
+        const int t = int(task >> 1);
+        const bool is_v = task & 1;
+        int64_t row;
+        if (!row_place(s, t, nullptr, false, row) || row < 0) continue;
+        const int64_t sh = is_v ? vsh : ksh, src = int64_t(t) * (is_v ? vst : kst);
+        const void *in = is_v ? v : k;
+        uint32_t *codes = is_v ? vc : kc;
+        uint8_t *scales = is_v ? vs : ks;
+        for (int p0 = lane; p0 - lane < pieces; p0 += 32 * kPieces) {
+            float x[kPieces][8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float4 a = __ldg(p + q);
-                x[4 * q] = a.x;
-                x[4 * q + 1] = a.y;
-                x[4 * q + 2] = a.z;
-                x[4 * q + 3] = a.w;
+            for (int i = 0; i < kPieces; ++i) {
+                const int p = p0 + 32 * i, h = p / PH, c = p % PH;
+                const int64_t at = src + int64_t(h) * sh + 8 * c;
+                if (p < pieces) {
+                    if constexpr (F32) {
+                        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(in) + at);
+                        const float4 u = __ldg(q), w = __ldg(q + 1);
+                        x[i][0] = u.x, x[i][1] = u.y, x[i][2] = u.z, x[i][3] = u.w;
+                        x[i][4] = w.x, x[i][5] = w.y, x[i][6] = w.z, x[i][7] = w.w;
+                    } else {
+                        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(in) + at));
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[i][2 * e] = bf16_lo(w[e]), x[i][2 * e + 1] = bf16_hi(w[e]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
+                }
             }
-        } else {
-            uint4 raw[4];
-            load_block(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(is_v ? v : k) + off), 0, raw);
-            unpack32(raw, x);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int p = p0 + 32 * i, h = p / PH, c = p % PH;
+                uint32_t top = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7fffffffu);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                if (p >= pieces) continue;
+                uint32_t sb = 0xFFu, w = 0;
+                if (top < 0x7f800000u) {
+                    sb = e8m0_byte(__uint_as_float(top));
+                    const float f = inv_scale(sb);
+                    w = cvt_e2m1x8(x[i][0] * f, x[i][1] * f, x[i][2] * f, x[i][3] * f, x[i][4] * f, x[i][5] * f, x[i][6] * f,
+                                   x[i][7] * f);
+                }
+                const int64_t to = row + int64_t(h) * s.page;
+                codes[to * PH + c] = w;
+                if (c % 4 == 0) scales[to * NB + c / 4] = uint8_t(sb);
+            }
         }
-        uint4 c;
-        uint32_t sb;
-        mx_quantize_block(x, c, sb);
-        (is_v ? vc : kc)[row * nb + j] = c;
-        (is_v ? vs : ks)[row * nb + j] = uint8_t(sb);
     }
 }
 
 // Positions starts[b] + (row - cu[b]) of every sequence, decoded to bf16
 // (exact but for overflow: two significant bits times a power of two) or
-// fp32.  One thread per 32-block and array.  Rows that the table names no
-// page for come out as zeros.
-template <bool F32>
+// fp32.  Rows that the table names no page for come out as zeros.
+template <bool F32, int NB>
 __global__ void __launch_bounds__(kThreads)
-read_kernel(const uint4 *__restrict__ kc, const uint8_t *__restrict__ ks, const uint4 *__restrict__ vc,
+read_kernel(const uint32_t *__restrict__ kc, const uint8_t *__restrict__ ks, const uint32_t *__restrict__ vc,
             const uint8_t *__restrict__ vs, const int32_t *__restrict__ starts, void *__restrict__ out_k,
-            void *__restrict__ out_v, Seqs s, int nb)
+            void *__restrict__ out_v, Seqs s)
 {
     pdl_wait();
-    const int per_row = s.heads * nb;
-    const int64_t total = int64_t(s.T) * 2 * per_row;
-    const int64_t stride = int64_t(gridDim.x) * kThreads;
-    for (int64_t g = int64_t(blockIdx.x) * kThreads + threadIdx.x; g < total; g += stride) {
-        const int t = int(g / (2 * per_row));
-        int r = int(g - int64_t(t) * (2 * per_row));
-        const bool is_v = r >= per_row;
-        if (is_v) r -= per_row;
-        const int h = r / nb, j = r - h * nb;
-        const int b = seq_of_row(s, t);
-        if (b < 0) continue;
-        int lo, hi;
-        seq_rows(s, b, lo, hi);
-        const int64_t row = cache_row(s, b, h, int64_t(t - lo) + (starts ? __ldg(starts + b) : 0));
-        uint4 c = make_uint4(0u, 0u, 0u, 0u);
-        float sc = 0.0f;
-        if (row >= 0) {
-            c = __ldg((is_v ? vc : kc) + row * nb + j);
-            sc = e8m0_value(__ldg((is_v ? vs : ks) + row * nb + j));
-        }
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-        const int64_t off = int64_t(t) * per_row + r;
+    constexpr int PH = 4 * NB;
+    const int lane = threadIdx.x % 32, pieces = s.heads * PH;
+    const int64_t warps = int64_t(gridDim.x) * (kThreads / 32);
+    for (int64_t task = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; task < 2 * int64_t(s.T); task += warps) {
+        const int t = int(task >> 1);
+        const bool is_v = task & 1;
+        int64_t row;
+        if (!row_place(s, t, starts, true, row)) continue;
+        const uint32_t *codes = is_v ? vc : kc;
+        const uint8_t *scales = is_v ? vs : ks;
         void *out = is_v ? out_v : out_k;
+        for (int p0 = lane; p0 < pieces; p0 += 32 * kPieces) {
+            uint32_t w[kPieces], sb[kPieces];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float2 e[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                e[i] = e2m1x2_to_f32x2((w[q] >> (8 * i)) & 0xFFu);
-                e[i].x *= sc;
-                e[i].y *= sc;
+            for (int i = 0; i < kPieces; ++i) {
+                const int p = p0 + 32 * i, h = p / PH, c = p % PH;
+                w[i] = sb[i] = 0;
+                if (p < pieces && row >= 0) {
+                    const int64_t at = row + int64_t(h) * s.page;
+                    w[i] = __ldg(codes + at * PH + c);
+                    sb[i] = __ldg(scales + at * NB + c / 4);
+                }
             }
-            if constexpr (F32) {
-                float4 *o = static_cast<float4 *>(out) + off * 8 + 2 * q;
-                o[0] = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
-                o[1] = make_float4(e[2].x, e[2].y, e[3].x, e[3].y);
-            } else {
-                static_cast<uint4 *>(out)[off * 4 + q] =
-                    make_uint4(mma::pack_bf16x2(e[0].x, e[0].y), mma::pack_bf16x2(e[1].x, e[1].y),
-                               mma::pack_bf16x2(e[2].x, e[2].y), mma::pack_bf16x2(e[3].x, e[3].y));
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int p = p0 + 32 * i;
+                if (p >= pieces) break;
+                const float f = e8m0_value(sb[i]);
+                float2 e[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    e[j] = e2m1x2_to_f32x2((w[i] >> (8 * j)) & 0xFFu);
+                    e[j].x *= f;
+                    e[j].y *= f;
+                }
+                const int64_t to = int64_t(t) * pieces + p;
+                if constexpr (F32) {
+                    float4 *o = static_cast<float4 *>(out) + to * 2;
+                    o[0] = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
+                    o[1] = make_float4(e[2].x, e[2].y, e[3].x, e[3].y);
+                } else {
+                    static_cast<uint4 *>(out)[to] =
+                        make_uint4(mma::pack_bf16x2(e[0].x, e[0].y), mma::pack_bf16x2(e[1].x, e[1].y),
+                                   mma::pack_bf16x2(e[2].x, e[2].y), mma::pack_bf16x2(e[3].x, e[3].y));
+                }
             }
         }
     }
