@@ -282,9 +282,13 @@ int mxf4_gemm_variant(int variant, const uint8_t *a_codes, const uint8_t *a_sf,
  * 2^-32 of the largest of them, which are off by at most 2^-40 of it); products
  * are exact.  Needs 0 <= M <= 32, K a positive multiple of 32, N, K < 2^31; any N;
  * pointers 16-byte aligned, ldx >= K a multiple of 8 (not read for M = 1); out may not overlap the
- * inputs.  A scale byte 0xFF makes the outputs it reaches NaN. */
+ * inputs.  A scale byte 0xFF makes the outputs it reaches NaN.  workspace:
+ * mxf4_gemv_workspace bytes of device memory (0 for small products), not shared with another
+ * call in flight; its content does not matter. */
+int64_t mxf4_gemv_workspace(int64_t M, int64_t N, int64_t K);
 int mxf4_gemv(const void *x_bf16, int64_t ldx, const uint8_t *b_codes, const uint8_t *b_sf,
-              void *out, int out_f32, int64_t M, int64_t N, int64_t K, cudaStream_t stream);
+              void *out, int out_f32, int64_t M, int64_t N, int64_t K,
+              void *workspace, int64_t workspace_bytes, cudaStream_t stream);
 
 /* A paged MXFP4 cache of one layer's keys and values.  Page p holds
  * page_size positions of each of the `heads` kv heads:

@@ -34,8 +34,8 @@ def err(L):
 
 
 def test_gemv_refusals(L):
-    def call(x=16, ldx=64, c=16, s=16, o=16, M=2, N=8, K=64):
-        return L.mxf4_gemv(P(x), ldx, P(c), P(s), P(o), 0, M, N, K, None)
+    def call(x=16, ldx=64, c=16, s=16, o=16, M=2, N=8, K=64, ws=None, n=0):
+        return L.mxf4_gemv(P(x), ldx, P(c), P(s), P(o), 0, M, N, K, P(ws), n, None)
 
     assert call(M=33) == -2 and "mxf4_gemm" in err(L)
     assert call(M=-1) == -2 and call(N=-1) == -2 and call(K=48) == -2 and call(K=0) == -2
@@ -45,6 +45,13 @@ def test_gemv_refusals(L):
     assert call(x=8) == -3 and call(c=8) == -3 and call(s=4) == -3 and call(o=8) == -3 and call(ldx=68) == -3
     assert call(x=None, c=None, s=None, o=None, M=0) == 0 and call(x=None, c=None, s=None, o=None, N=0) == 0
     assert err(L) == ""
+    big = dict(M=9, N=1 << 20, K=1 << 12, ldx=1 << 12)
+    need = L.mxf4_gemv_workspace(9, 1 << 20, 1 << 12)
+    assert need > 0 and L.mxf4_gemv_workspace(2, 8, 64) == 0 and L.mxf4_gemv_workspace(0, 1 << 20, 1 << 12) == 0
+    assert call(**big, ws=16, n=need - 1) == -2 and "workspace" in err(L)
+    assert call(**big, n=need) == -1 and call(**big, ws=8, n=need) == -3
+    for bad in ((33, 8, 64), (-1, 8, 64), (2, -1, 64), (2, 8, 48), (2, 8, 0), (2, 1 << 31, 64)):
+        assert L.mxf4_gemv_workspace(*bad) == -1
 
 
 SHAPES = [dict(d=48), dict(d=160), dict(d=0), dict(heads=0), dict(heads=65536), dict(page=8), dict(page=24), dict(page=0),

@@ -41,7 +41,7 @@ __all__ = [
     "kq_transform_f32_variant", "kq_quantize_lu", "fwht_quantize", "kq_inverse_f32", "mx_dequantize", "norm_kq_quantize",
     "KQ_SCALES_ROWMAJOR", "KQ_SCALES_SF", "kq_sf_bytes", "kq_quantize_sf", "mx_quantize_f32", "mx_scales_to_sf",
     "mxf4_gemm", "mxf4_gemm_variant", "norm_kq_quantize_sf", "norm_kq_quantize_variant",
-    "mxf4_gemv", "mx_cache_write", "mx_cache_read", "mx_paged_attention", "mx_attention_workspace",
+    "mxf4_gemv", "mxf4_gemv_workspace", "mx_cache_write", "mx_cache_read", "mx_paged_attention", "mx_attention_workspace",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkroquant.so")
@@ -71,7 +71,7 @@ _SIGS = {
     "mx_scales_to_sf": "ppqqp",
     "mxf4_gemm": "pppppiqqqp",
     "mxf4_gemm_variant": "ipppppiqqqp",
-    "mxf4_gemv": "pqpppiqqqp",
+    "mxf4_gemv": "pqpppiqqqpqp",
     "mx_cache_write": "pqqpqqippqp",
     "mx_cache_read": "pppppiqp",
     "mx_paged_attention": "pqqppfipqqqpqp",
@@ -118,6 +118,8 @@ def lib() -> ctypes.CDLL:
         L.norm_kq_quantize_variant.restype = ctypes.c_int
         L.kq_sf_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64]
         L.kq_sf_bytes.restype = ctypes.c_int64
+        L.mxf4_gemv_workspace.argtypes = [ctypes.c_int64] * 3
+        L.mxf4_gemv_workspace.restype = ctypes.c_int64
         L.mx_attention_workspace.argtypes = [ctypes.c_int64] * 5
         L.mx_attention_workspace.restype = ctypes.c_int64
         _lib = L
@@ -549,11 +551,20 @@ def norm_kq_quantize_sf(h, gamma, beta, factors, eps=1e-6, shared=False, out_cod
     return out_codes, out_sf
 
 
-def mxf4_gemv(x, b_codes, b_sf, out=None, out_dtype=None, stream=None):
+def mxf4_gemv_workspace(M: int, N: int, K: int) -> int:
+    """Bytes of workspace that mxf4_gemv needs for calls of these sizes."""
+    n = lib().mxf4_gemv_workspace(int(M), int(N), int(K))
+    if n < 0:
+        raise ValueError(f"mxf4_gemv_workspace: bad sizes {M}, {N}, {K}")
+    return n
+
+
+def mxf4_gemv(x, b_codes, b_sf, out=None, out_dtype=None, workspace=None, stream=None):
     """A few rows times MXFP4 weights: out[m, n] = sum_k x[m, k] b[n, k], M <= 32.
 
     x bf16 [M, K] (rows may be strided), not quantized; b_codes [N, K/2] and b_sf the
-    weight operand of mxf4_gemm; out bf16 (default) or float32 [M, N].
+    weight operand of mxf4_gemm; out bf16 (default) or float32 [M, N].  workspace: uint8
+    tensor of mxf4_gemv_workspace(M, N, K) bytes for this call alone; allocated if None.
     """
     torch = _torch()
     _need_rows(x, "x", (torch.bfloat16,), 2)
@@ -569,8 +580,14 @@ def mxf4_gemv(x, b_codes, b_sf, out=None, out_dtype=None, stream=None):
     if out.dtype not in (torch.bfloat16, torch.float32) or (out_dtype is not None and out.dtype != out_dtype):
         raise TypeError(f"out must be {out_dtype or 'bfloat16 or float32'}, got {out.dtype}")
     _need(out, "out", out.dtype, dev, (M, N))
+    need = lib().mxf4_gemv_workspace(M, N, K)                # -1: sizes that the call refuses
+    if workspace is None and need > 0:
+        workspace = _scratch(need, dev, stream)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, dev)
     _call("mxf4_gemv", dev, _ptr(x), x.stride(0) if M > 1 else K, _ptr(b_codes), _ptr(b_sf), _ptr(out),
-          int(out.dtype == torch.float32), M, N, K, _stream(stream, dev))
+          int(out.dtype == torch.float32), M, N, K, _ptr(workspace), 0 if workspace is None else workspace.numel(),
+          _stream(stream, dev))
     return out
 
 

@@ -2783,30 +2783,45 @@ struct GemvArgs {
     const __nv_bfloat16 *x;
     int64_t ldx;
     const uint8_t *codes, *sf;
+    uint8_t *xw;                             // workspace
     void *out;
     int M, N, K;
     cudaStream_t stream;
 };
 
-template <int RT, int NT, bool F32>
+// Whether x is converted by a kernel of its own.  Measured, us with and without
+// (GPU time): 16 x 1152 x 1152 6.5 / 8.5, 32 x 8192 x 28672 88 / 180, 8 x 4096 x
+// 4096 8.5 / 11.1, 8 x 1152 x 1152 5.5 / 4.9, 1 x 8192 x 28672 38.5 / 34.3: with
+// more than 8 rows always, with more than 4 from kGemvPre pieces of 128 weight
+// rows x 256 channels.
+constexpr int64_t kGemvPre = 256;
+
+template <int RT, int NT, bool PRE, bool F32>
 std::atomic<int> g_gemv_set[kMaxDevices];
 
-template <int RT, int NT, bool F32>
+template <int RT, int NT, bool PRE, bool F32>
 int gemv_launch(const char *fn, const GemvArgs &a, int parts, int S)
 {
-    auto k = gemv::mxf4_gemv_kernel<RT, NT, F32>;
+    auto k = gemv::mxf4_gemv_kernel<RT, NT, PRE, F32>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
-    if (dev < 0 || dev >= kMaxDevices || !g_gemv_set<RT, NT, F32>[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(gemv::kSmem<NT>));
+    if (dev < 0 || dev >= kMaxDevices || !g_gemv_set<RT, NT, PRE, F32>[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(gemv::kSmem<RT, NT, PRE>));
         if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        if (dev >= 0 && dev < kMaxDevices) g_gemv_set<RT, NT, F32>[dev].store(1, std::memory_order_release);
+        if (dev >= 0 && dev < kMaxDevices) g_gemv_set<RT, NT, PRE, F32>[dev].store(1, std::memory_order_release);
+    }
+    if constexpr (PRE) {
+        const int nb = a.K / 32, KC = (nb + gemv::kChunkBlocks - 1) / gemv::kChunkBlocks;
+        launch(gemv::convert_kernel, unsigned((int64_t(KC) * 8 * NT + 7) / 8), 256, 0, a.stream, a.x, a.ldx, a.xw, a.M,
+               8 * NT, nb, KC);
+        const int rc = launch_check(fn);
+        if (rc != KQ_OK) return rc;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(parts * S), 1, 1);
     cfg.blockDim = dim3(gemv::kWarps * 32, 1, 1);
-    cfg.dynamicSmemBytes = gemv::kSmem<NT>;
+    cfg.dynamicSmemBytes = gemv::kSmem<RT, NT, PRE>;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -2817,8 +2832,16 @@ int gemv_launch(const char *fn, const GemvArgs &a, int parts, int S)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = S > 1 ? 2 : 1;
-    (void)cudaLaunchKernelEx(&cfg, k, a.x, a.ldx, a.codes, a.sf, a.out, a.M, a.N, a.K, S);
+    (void)cudaLaunchKernelEx(&cfg, k, a.x, a.ldx, a.codes, a.sf, static_cast<const uint8_t *>(a.xw), a.out, a.M, a.N, a.K, S);
     return launch_check(fn);
+}
+
+// Row tiles of 8 rows for M rows, 0 for M = 0.
+int gemv_tiles(int64_t M) { return M <= 8 ? 1 : M <= 16 ? 2 : 4; }
+
+bool gemv_pre(int64_t M, int64_t N, int64_t K)
+{
+    return M > 8 || (M > 4 && (N + 127) / 128 * ((K + 255) / 256) >= kGemvPre);
 }
 
 // Row tiles per CTA and ranks per cluster.  A CTA's x is 2 M / (17/32 x 16 RT)
@@ -2828,7 +2851,6 @@ int gemv_launch(const char *fn, const GemvArgs &a, int parts, int S)
 template <int NT, bool F32>
 int gemv_rows(const char *fn, const GemvArgs &a, int sms)
 {
-    constexpr int kMinRT = NT == 1 ? 1 : NT;                 // the channel groups that a fill of x is made for
     const int groups = (a.N + 127) / 128, KC = (a.K / 32 + gemv::kChunkBlocks - 1) / gemv::kChunkBlocks;
     auto ranks = [&](int rt) {
         const int kg = gemv::kWarps / rt, parts = groups * kg;
@@ -2836,14 +2858,24 @@ int gemv_rows(const char *fn, const GemvArgs &a, int sms)
         while (S < 8 && int64_t(parts) * S * 2 <= 2 * sms && KC >= 2 * S * kg) S *= 2;
         return S;
     };
+    constexpr int kMinRT = NT;               // (what shared memory holds of x)
     int rt = 8;
     while (rt > kMinRT && int64_t(groups) * (gemv::kWarps / rt) * ranks(rt) < sms) rt /= 2;
     const int parts = groups * (gemv::kWarps / rt), S = ranks(rt);
-    switch (rt) {
-    case 8: return gemv_launch<8, NT, F32>(fn, a, parts, S);
-    case 4: return gemv_launch<4, NT, F32>(fn, a, parts, S);
-    case 2: if constexpr (kMinRT <= 2) return gemv_launch<2, NT, F32>(fn, a, parts, S); break;
-    default: if constexpr (kMinRT <= 1) return gemv_launch<1, NT, F32>(fn, a, parts, S); break;
+    if (NT > 1 || gemv_pre(a.M, a.N, a.K)) {
+        switch (rt) {
+        case 8: return gemv_launch<8, NT, true, F32>(fn, a, parts, S);
+        case 4: return gemv_launch<4, NT, true, F32>(fn, a, parts, S);
+        case 2: if constexpr (kMinRT <= 2) return gemv_launch<2, NT, true, F32>(fn, a, parts, S); break;
+        default: if constexpr (kMinRT <= 1) return gemv_launch<1, NT, true, F32>(fn, a, parts, S); break;
+        }
+    } else if constexpr (NT == 1) {
+        switch (rt) {
+        case 8: return gemv_launch<8, 1, false, F32>(fn, a, parts, S);
+        case 4: return gemv_launch<4, 1, false, F32>(fn, a, parts, S);
+        case 2: return gemv_launch<2, 1, false, F32>(fn, a, parts, S);
+        default: return gemv_launch<1, 1, false, F32>(fn, a, parts, S);
+        }
     }
     return fail(KQ_ERR_VARIANT, "%s: no such row tile", fn);
 }
@@ -2854,9 +2886,11 @@ int gemv_dispatch(const char *fn, const GemvArgs &a)
     int sms = 0;
     int rc = sm_count(&sms);
     if (rc != KQ_OK) return rc;
-    if (a.M <= 8) return gemv_rows<1, F32>(fn, a, sms);
-    if (a.M <= 16) return gemv_rows<2, F32>(fn, a, sms);
-    return gemv_rows<4, F32>(fn, a, sms);
+    switch (gemv_tiles(a.M)) {
+    case 1: return gemv_rows<1, F32>(fn, a, sms);
+    case 2: return gemv_rows<2, F32>(fn, a, sms);
+    default: return gemv_rows<4, F32>(fn, a, sms);
+    }
 }
 
 // --- attention over the cache ---
@@ -3338,8 +3372,16 @@ int kq_fold_weights(const float *W, const float *factors, int shared, float *W_o
     return launch_check("kq_fold_weights");
 }
 
+int64_t mxf4_gemv_workspace(int64_t M, int64_t N, int64_t K)
+{
+    if (M < 0 || M > gemv::kMaxRows || N < 0 || N >= (int64_t(1) << 31) || K <= 0 || K % kBlk != 0 || K >= (int64_t(1) << 31))
+        return -1;
+    if (M == 0 || N == 0 || !gemv_pre(M, N, K)) return 0;
+    return gemv::x_bytes((K / 32 + gemv::kChunkBlocks - 1) / gemv::kChunkBlocks, 8 * gemv_tiles(M));
+}
+
 int mxf4_gemv(const void *x_bf16, int64_t ldx, const uint8_t *b_codes, const uint8_t *b_sf, void *out, int out_f32,
-              int64_t M, int64_t N, int64_t K, cudaStream_t stream)
+              int64_t M, int64_t N, int64_t K, void *workspace, int64_t workspace_bytes, cudaStream_t stream)
 {
     const char *fn = "mxf4_gemv";
     if (M < 0 || M > gemv::kMaxRows || N < 0 || K <= 0 || K % kBlk != 0)
@@ -3354,7 +3396,14 @@ int mxf4_gemv(const void *x_bf16, int64_t ldx, const uint8_t *b_codes, const uin
     if (!aligned(x_bf16, 16) || !aligned(b_codes, 16) || !aligned(b_sf, 16) || !aligned(out, 16) ||
         (M > 1 && ldx % 8 != 0))
         return fail(KQ_ERR_ALIGN, "%s: every pointer must be 16-byte aligned and ldx a multiple of 8", fn);
-    const GemvArgs a{static_cast<const __nv_bfloat16 *>(x_bf16), ldx, b_codes, b_sf, out, int(M), int(N), int(K), stream};
+    const int64_t need = mxf4_gemv_workspace(M, N, K);
+    if (workspace_bytes < need)
+        return fail(KQ_ERR_SHAPE, "%s: workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes,
+                    (long long)need);
+    if (need > 0 && !workspace) return fail(KQ_ERR_NULL, "%s: NULL pointer argument (workspace)", fn);
+    if (!aligned(workspace, 16)) return fail(KQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+    const GemvArgs a{static_cast<const __nv_bfloat16 *>(x_bf16), ldx, b_codes, b_sf, static_cast<uint8_t *>(workspace), out,
+                     int(M), int(N), int(K), stream};
     return out_f32 ? gemv_dispatch<true>(fn, a) : gemv_dispatch<false>(fn, a);
 }
 

@@ -29,11 +29,14 @@
 // 128-row scale group and their 4 quarters (rows base + 32 q + l), so that its
 // scales of 128 channels are 64 consecutive bytes.  A stage is 256 channels:
 // 16 rows x 128 bytes of codes and 2 x 64 of scales, brought by cp.async into
-// the warp's own ring of kStages (nothing but the warp waits for it), the
+// the warp's own ring (nothing but the warp waits for it), the
 // 16-byte pieces xor-swizzled by row, so that the 4-byte reads of 8 rows x 4
 // words are conflict-free.  A CTA is 8 warps: RT row tiles x 8 / RT groups of
 // channels; x is converted once per CTA for `kXChunks` chunks at a time and
-// shared by all warps.  The channels are also split over the CTAs of a
+// shared by all warps.  Where that conversion is a good part of the work (many
+// rows, or many CTAs converting the same x) a kernel of its own does it once, in
+// the layout that the product reads, and x comes by cp.async with the weights,
+// the chunks of a stage for all of the CTA's warps (PRE).  The channels are also split over the CTAs of a
 // cluster (up to 8), whose partial sums are added through distributed shared
 // memory in rank order: one launch, no workspace, the same bits every time.
 
@@ -41,13 +44,15 @@ namespace gemv {
 
 constexpr int kMaxRows = 32;
 constexpr int kWarps = 8;
-constexpr int kStages = 4;
+template <int NT>
+constexpr int kStages = NT == 4 ? 3 : 4;                      // (3: two CTAs of 32 rows fit on an SM, 32 x 4096 x 4096 24 -> 13 us)
 constexpr int kChunkBlocks = 8;                               // 32-blocks per stage (256 channels)
 constexpr int kCodeBytes = 16 * 16 * kChunkBlocks;            // 2048
 constexpr int kScaleBytes = 16 * kChunkBlocks;                // 128
 constexpr int kStageBytes = kCodeBytes + kScaleBytes;
 constexpr int kTableBytes = 16 * kChunkBlocks * 4;            // decoded scales of the current stage
-constexpr size_t kRing = size_t(kWarps) * (kStages * kStageBytes + kTableBytes);
+template <int NT>
+constexpr size_t kRing = size_t(kWarps) * (kStages<NT> * kStageBytes + kTableBytes);
 
 // Chunks of x held at once: 32 KB of fp16 whatever the number of rows.  A
 // block's rows are 64 bytes each, and 64 bytes of padding put two consecutive
@@ -60,7 +65,16 @@ template <int NT>
 constexpr int kXBytes = kXChunks<NT> * kChunkBlocks * kXBlockBytes<NT>;
 
 template <int NT>
-constexpr size_t kSmem = kRing + size_t(kXBytes<NT>) + size_t(kXChunks<NT>) * 8 * NT * 4;
+constexpr int kXStage = kChunkBlocks * kXBlockBytes<NT> + 8 * NT * 4;                    // PRE: a chunk and its exponents
+
+template <int RT, int NT, bool PRE>
+constexpr size_t kSmem = kRing<NT> + (PRE ? size_t(kStages<NT>) * kXStage<NT> * (kWarps / RT)
+                                          : size_t(kXBytes<NT>) + size_t(kXChunks<NT>) * 8 * NT * 4);
+
+// x converted beforehand: [K / 32, whole chunks][rows, 8 NT][32] fp16, then
+// [chunks][rows] fp32 exponents.
+__host__ __device__ constexpr int64_t x_elements(int64_t KC, int rows) { return KC * kChunkBlocks * rows * 32; }
+__host__ __device__ constexpr int64_t x_bytes(int64_t KC, int rows) { return x_elements(KC, rows) * 2 + KC * rows * 4; }
 
 // Copy `bytes` (16, or 0: src is not read) and fill up 16 bytes with zeros.
 __device__ __forceinline__ void cp_async16_sized(uint32_t dst, const void *src, uint32_t bytes)
@@ -148,6 +162,23 @@ __device__ __forceinline__ float4 scales4(uint32_t w)
     return make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
 }
 
+// A warp per row and chunk; rows M .. rows - 1 are zeros.
+__global__ void __launch_bounds__(256)
+convert_kernel(const __nv_bfloat16 *__restrict__ x, int64_t ldx, uint8_t *__restrict__ xw, int M, int rows, int nb, int KC)
+{
+    pdl_wait();
+    const int lane = threadIdx.x % 32;
+    const int64_t i = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
+    if (i >= int64_t(KC) * rows) return;
+    const int m = int(i % rows), ch = int(i / rows), blk = ch * kChunkBlocks + lane / 4;
+    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+    if (m < M && blk < nb) raw = __ldg(reinterpret_cast<const uint4 *>(x + m * ldx + int64_t(blk) * 32 + (lane % 4) * 8));
+    float e;
+    const uint4 h = x_chunk(raw, e);
+    reinterpret_cast<uint4 *>(xw)[(int64_t(blk) * rows + m) * 4 + lane % 4] = h;
+    if (lane == 0) reinterpret_cast<float *>(xw + x_elements(KC, rows) * 2)[int64_t(ch) * rows + m] = m < M ? e : 0.0f;
+}
+
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -166,25 +197,27 @@ __device__ __forceinline__ float cluster_load(const float *p, uint32_t rank)
 // Grid: (8 / RT parts of every 128-row group) x S ranks, rank fastest (a
 // cluster is the S ranks of one part).  Rank r takes chunks [r KC / S,
 // (r + 1) KC / S) of the KC = ceil(K / 256), in turn by the CTA's channel groups.
-template <int RT, int NT, bool F32OUT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 4 ? 1 : 2)
+template <int RT, int NT, bool PRE, bool F32OUT>
+__global__ void __launch_bounds__(kWarps * 32, 2)
 mxf4_gemv_kernel(const __nv_bfloat16 *__restrict__ x, int64_t ldx, const uint8_t *__restrict__ codes,
-                 const uint8_t *__restrict__ sf, void *__restrict__ out, int M, int N, int K, int S)
+                 const uint8_t *__restrict__ sf, const uint8_t *__restrict__ xw, void *__restrict__ out, int M, int N, int K,
+                 int S)
 {
     pdl_wait();
     constexpr int KG = kWarps / RT;                           // channel groups
     constexpr int kLanes = 4 * RT;                            // lanes l of the scale group per CTA
     constexpr int XC = kXChunks<NT>;
     constexpr int kRows = 16 * RT;
-    static_assert(XC % KG == 0, "a fill of x is whole rounds of the channel groups");
+    constexpr int ST = kStages<NT>;
+    static_assert(PRE || XC % KG == 0, "a fill of x is whole rounds of the channel groups");
     extern __shared__ __align__(16) uint8_t smem_dyn[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = lane / 4, c = lane % 4;
     const int rt = warp % RT, kg = warp / RT;
-    uint8_t *ring = smem_dyn + warp * (kStages * kStageBytes + kTableBytes);
-    float4 *table = reinterpret_cast<float4 *>(ring + kStages * kStageBytes);
-    uint8_t *xs = smem_dyn + kRing;                           // [blocks][8 NT rows of 64 bytes, padding]
-    float *xe = reinterpret_cast<float *>(xs + kXBytes<NT>);  // [XC][8 NT]
+    uint8_t *ring = smem_dyn + warp * (ST * kStageBytes + kTableBytes);
+    float4 *table = reinterpret_cast<float4 *>(ring + ST * kStageBytes);
+    uint8_t *xs = smem_dyn + kRing<NT>;                         // [blocks][8 NT rows of 64 bytes, padding]
+    float *xe = reinterpret_cast<float *>(xs + kXBytes<NT>);  // [XC][8 NT] (both: not with PRE)
 
     const int part = int(blockIdx.x) / S, rank = int(blockIdx.x) % S;
     const int group = part / KG, l0 = (part % KG) * kLanes + 4 * rt;       // the warp's lanes: l0 .. l0 + 3
@@ -223,6 +256,23 @@ mxf4_gemv_kernel(const __nv_bfloat16 *__restrict__ x, int64_t ldx, const uint8_t
             }
             ssrc += KG * 1024;
         }
+        if constexpr (PRE) {                                  // the CTA's threads bring the chunks of x together
+#pragma unroll
+            for (int kk = 0; kk < KG; ++kk) {
+                const int cx = ch - kg + kk;
+                if (cx >= c1) break;
+                const uint32_t to = smem_addr(xs) + (slot * KG + kk) * kXStage<NT>;
+                const uint8_t *from = xw + int64_t(cx) * kChunkBlocks * 8 * NT * 64;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {                // 256 NT pieces, 32 NT to a block
+                    const int i = threadIdx.x + 256 * j;
+                    cp_async16_sized(to + i / (32 * NT) * kXBlockBytes<NT> + i % (32 * NT) * 16, from + i * 16, 16);
+                }
+                if (threadIdx.x < 2 * NT)
+                    cp_async16_sized(to + kChunkBlocks * kXBlockBytes<NT> + threadIdx.x * 16,
+                                     xw + x_elements(KC, 8 * NT) * 2 + int64_t(cx) * 8 * NT * 4 + threadIdx.x * 16, 16);
+            }
+        }
         cp_commit();
     };
 
@@ -233,87 +283,101 @@ mxf4_gemv_kernel(const __nv_bfloat16 *__restrict__ x, int64_t ldx, const uint8_t
         for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
 
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(c0 + i * KG + kg, i);
-    // columns of no row stay zero
-    for (int i = threadIdx.x; i < XC * kChunkBlocks * 8 * NT * 4; i += kWarps * 32) {
-        const int m = i / 4 % (8 * NT), j = i / (32 * NT);
-        if (m >= M) *reinterpret_cast<uint4 *>(xs + j * kXBlockBytes<NT> + m * 64 + (i % 4) * 16) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (threadIdx.x < XC * 8 * NT) xe[threadIdx.x] = 0.0f;
-    int it = 0;
-    for (int f0 = c0; f0 < c1; f0 += XC) {
-        // ---- the next XC chunks of x, a row's chunk per warp and turn
-        __syncthreads();
-#pragma unroll 4
-        for (int i = warp; i < XC * M; i += kWarps) {
-            const int cc = i % XC, m = i / XC, blk = (f0 + cc) * kChunkBlocks + lane / 4;
-            if ((f0 + cc) * kChunkBlocks >= nb) continue;
-            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-            if (blk < nb)
-                raw = __ldg(reinterpret_cast<const uint4 *>(x + m * ldx + int64_t(blk) * 32 + (lane % 4) * 8));
-            float e;
-            const uint4 h = x_chunk(raw, e);
-            *reinterpret_cast<uint4 *>(xs + (cc * kChunkBlocks + lane / 4) * kXBlockBytes<NT> + m * 64 + (lane % 4) * 16) = h;
-            if (lane == 0) xe[cc * 8 * NT + m] = e;
+    for (int i = 0; i < ST - 1; ++i) fetch(c0 + i * KG + kg, i);
+    // chunk ch of the stage at `st` times x at `xc` with the exponents `ex`
+    auto product = [&](int ch, const uint8_t *st, const uint8_t *xc, const float *ex) {
+        {
+            // the stage's 128 scales as floats, [unit][row][4]: lane = unit * 16 + (l * 4 + quarter)
+            const uint32_t w = reinterpret_cast<const uint32_t *>(st + kCodeBytes)[lane];
+            float4 s = scales4(w);
+            const int left = nb - (ch * kChunkBlocks + (lane / 16) * 4);
+            if (left < 4) {                               // padding bytes of the last unit may hold anything
+                if (left < 1) s.x = 0.0f;
+                if (left < 2) s.y = 0.0f;
+                if (left < 3) s.z = 0.0f;
+                s.w = 0.0f;
+            }
+            table[(lane & 16) + (lane & 3) * 4 + ((lane >> 2) & 3)] = s;
         }
-        __syncthreads();
-        const int f1 = min(c1, f0 + XC);
-        for (int ch = f0 + kg; ch < f1; ch += KG, ++it) {
-            cp_wait<kStages - 2>();
-            __syncwarp();
-            fetch(ch + (kStages - 1) * KG, (it + kStages - 1) % kStages);
-            const uint8_t *st = ring + (it % kStages) * kStageBytes;
-            {
-                // the stage's 128 scales as floats, [unit][row][4]: lane = unit * 16 + (l * 4 + quarter)
-                const uint32_t w = reinterpret_cast<const uint32_t *>(st + kCodeBytes)[lane];
-                float4 s = scales4(w);
-                const int left = nb - (ch * kChunkBlocks + (lane / 16) * 4);
-                if (left < 4) {                               // padding bytes of the last unit may hold anything
-                    if (left < 1) s.x = 0.0f;
-                    if (left < 2) s.y = 0.0f;
-                    if (left < 3) s.z = 0.0f;
-                    s.w = 0.0f;
-                }
-                table[(lane & 16) + (lane & 3) * 4 + ((lane >> 2) & 3)] = s;
-            }
-            __syncwarp();
-            const uint8_t *xc = xs + (ch - f0) * kChunkBlocks * kXBlockBytes<NT> + g * 64 + c * 16;
-            float sum[NT][4];
+        __syncwarp();
+        xc += g * 64 + c * 16;
+        float sum[NT][4];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum[t][i] = 0.0f;
+            for (int i = 0; i < 4; ++i) sum[t][i] = 0.0f;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float4 t0 = table[u * 16 + g], t1 = table[u * 16 + g + 8];
-                const float lo[4] = {t0.x, t0.y, t0.z, t0.w}, hi[4] = {t1.x, t1.y, t1.z, t1.w};
+        for (int u = 0; u < 2; ++u) {
+            const float4 t0 = table[u * 16 + g], t1 = table[u * 16 + g + 8];
+            const float lo[4] = {t0.x, t0.y, t0.z, t0.w}, hi[4] = {t1.x, t1.y, t1.z, t1.w};
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int j = 4 * u + b;
-                    const uint8_t *row = st + g * 128 + ((j ^ g) << 4) + c * 4;
-                    uint32_t a[4], d[4];
-                    codes_f16(*reinterpret_cast<const uint32_t *>(row), a);
-                    codes_f16(*reinterpret_cast<const uint32_t *>(row + 8 * 128), d);
+            for (int b = 0; b < 4; ++b) {
+                const int j = 4 * u + b;
+                const uint8_t *row = st + g * 128 + ((j ^ g) << 4) + c * 4;
+                uint32_t a[4], d[4];
+                codes_f16(*reinterpret_cast<const uint32_t *>(row), a);
+                codes_f16(*reinterpret_cast<const uint32_t *>(row + 8 * 128), d);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const uint4 bx = *reinterpret_cast<const uint4 *>(xc + j * kXBlockBytes<NT> + t * 512);
-                        float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma_f16(p, a[0], d[0], a[1], d[1], bx.x, bx.y);
-                        mma_f16(p, a[2], d[2], a[3], d[3], bx.z, bx.w);
-                        sum[t][0] = fmaf(p[0], lo[b], sum[t][0]);
-                        sum[t][1] = fmaf(p[1], lo[b], sum[t][1]);
-                        sum[t][2] = fmaf(p[2], hi[b], sum[t][2]);
-                        sum[t][3] = fmaf(p[3], hi[b], sum[t][3]);
-                    }
+                for (int t = 0; t < NT; ++t) {
+                    const uint4 bx = *reinterpret_cast<const uint4 *>(xc + j * kXBlockBytes<NT> + t * 512);
+                    float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma_f16(p, a[0], d[0], a[1], d[1], bx.x, bx.y);
+                    mma_f16(p, a[2], d[2], a[3], d[3], bx.z, bx.w);
+                    sum[t][0] = fmaf(p[0], lo[b], sum[t][0]);
+                    sum[t][1] = fmaf(p[1], lo[b], sum[t][1]);
+                    sum[t][2] = fmaf(p[2], hi[b], sum[t][2]);
+                    sum[t][3] = fmaf(p[3], hi[b], sum[t][3]);
                 }
             }
+        }
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const float2 e = *reinterpret_cast<const float2 *>(xe + (ch - f0) * 8 * NT + 8 * t + 2 * c);
-                acc[t][0] = fmaf(sum[t][0], e.x, acc[t][0]);
-                acc[t][1] = fmaf(sum[t][1], e.y, acc[t][1]);
-                acc[t][2] = fmaf(sum[t][2], e.x, acc[t][2]);
-                acc[t][3] = fmaf(sum[t][3], e.y, acc[t][3]);
+        for (int t = 0; t < NT; ++t) {
+            const float2 e = *reinterpret_cast<const float2 *>(ex + 8 * t + 2 * c);
+            acc[t][0] = fmaf(sum[t][0], e.x, acc[t][0]);
+            acc[t][1] = fmaf(sum[t][1], e.y, acc[t][1]);
+            acc[t][2] = fmaf(sum[t][2], e.x, acc[t][2]);
+            acc[t][3] = fmaf(sum[t][3], e.y, acc[t][3]);
+        }
+    };
+    if constexpr (PRE) {
+        for (int ch = c0 + kg, it = 0; ch - kg < c1; ch += KG, ++it) {
+            cp_wait<ST - 2>();
+            __syncthreads();                                  // everybody's pieces are there, the stage before is free
+            fetch(ch + (ST - 1) * KG, (it + ST - 1) % ST);
+            const uint8_t *xc = xs + (it % ST * KG + kg) * kXStage<NT>;
+            if (ch < c1)
+                product(ch, ring + (it % ST) * kStageBytes, xc, reinterpret_cast<const float *>(xc + kChunkBlocks * kXBlockBytes<NT>));
+        }
+    } else {
+        // columns of no row stay zero
+        for (int i = threadIdx.x; i < XC * kChunkBlocks * 8 * NT * 4; i += kWarps * 32) {
+            const int m = i / 4 % (8 * NT), j = i / (32 * NT);
+            if (m >= M) *reinterpret_cast<uint4 *>(xs + j * kXBlockBytes<NT> + m * 64 + (i % 4) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (threadIdx.x < XC * 8 * NT) xe[threadIdx.x] = 0.0f;
+        int it = 0;
+        for (int f0 = c0; f0 < c1; f0 += XC) {
+            // ---- the next XC chunks of x, a row's chunk per warp and turn
+            __syncthreads();
+#pragma unroll 4
+            for (int i = warp; i < XC * M; i += kWarps) {
+                const int cc = i % XC, m = i / XC, blk = (f0 + cc) * kChunkBlocks + lane / 4;
+                if ((f0 + cc) * kChunkBlocks >= nb) continue;
+                uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                if (blk < nb)
+                    raw = __ldg(reinterpret_cast<const uint4 *>(x + m * ldx + int64_t(blk) * 32 + (lane % 4) * 8));
+                float e;
+                const uint4 h = x_chunk(raw, e);
+                *reinterpret_cast<uint4 *>(xs + (cc * kChunkBlocks + lane / 4) * kXBlockBytes<NT> + m * 64 + (lane % 4) * 16) = h;
+                if (lane == 0) xe[cc * 8 * NT + m] = e;
+            }
+            __syncthreads();
+            const int f1 = min(c1, f0 + XC);
+            for (int ch = f0 + kg; ch < f1; ch += KG, ++it) {
+                cp_wait<ST - 2>();
+                __syncwarp();
+                fetch(ch + (ST - 1) * KG, (it + ST - 1) % ST);
+                product(ch, ring + (it % ST) * kStageBytes, xs + (ch - f0) * kChunkBlocks * kXBlockBytes<NT>, xe + (ch - f0) * 8 * NT);
             }
         }
     }
