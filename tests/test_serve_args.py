@@ -22,11 +22,11 @@ def L():
 
 
 def cache(pages=4, heads=2, page=16, d=64, kc=16, ks=16, vc=16, vs=16):
-    return kq._Cache(kc, ks, vc, vs, pages, heads, page, d)
+    return kq._CACHE.pack(kc or 0, ks or 0, vc or 0, vs or 0, pages, heads, page, d)
 
 
 def batch(table=16, stride=3, pages=3, cu=16, lens=16, B=2):
-    return kq._Batch(table, stride, pages, cu, lens, B)
+    return kq._BATCH.pack(table or 0, stride, pages, cu or 0, lens or 0, B)
 
 
 def err(L):
@@ -60,15 +60,15 @@ BATCHES = [dict(B=-1), dict(pages=-1), dict(pages=4), dict(stride=1 << 32, pages
 
 
 def write(L, c, b, k=16, v=16, st=128, sh=64, f32=0, T=4):
-    return L.mx_cache_write(P(k), st, sh, P(v), st, sh, f32, ctypes.addressof(c), ctypes.addressof(b), T, None)
+    return L.mx_cache_write(P(k), st, sh, P(v), st, sh, f32, c, b, T, None)
 
 
 def read(L, c, b, k=16, v=16, starts=None, T=4):
-    return L.mx_cache_read(ctypes.addressof(c), ctypes.addressof(b), P(starts), P(k), P(v), 0, T, None)
+    return L.mx_cache_read(c, b, P(starts), P(k), P(v), 0, T, None)
 
 
 def attend(L, c, b, q=16, st=256, sh=64, o=16, T=4, hq=4, max_new=1, scale=1.0, ws=1024, n=1 << 40, causal=1):
-    return L.mx_paged_attention(P(q), st, sh, ctypes.addressof(c), ctypes.addressof(b), scale, causal, P(o), T, hq, max_new,
+    return L.mx_paged_attention(P(q), st, sh, c, b, scale, causal, P(o), T, hq, max_new,
                                 P(ws), n, None)
 
 
@@ -90,8 +90,8 @@ def test_shared_refusals(L, fn):
 
 def test_null_structs(L):
     c, b = cache(), batch()
-    assert L.mx_cache_write(P(16), 128, 64, P(16), 128, 64, 0, None, ctypes.addressof(b), 4, None) == -1
-    assert L.mx_cache_read(ctypes.addressof(c), None, None, P(16), P(16), 0, 4, None) == -1
+    assert L.mx_cache_write(P(16), 128, 64, P(16), 128, 64, 0, None, b, 4, None) == -1
+    assert L.mx_cache_read(c, None, None, P(16), P(16), 0, 4, None) == -1
     assert L.mx_paged_attention(P(16), 256, 64, None, None, 1.0, 1, P(16), 4, 4, 1, None, 0, None) == -1
 
 

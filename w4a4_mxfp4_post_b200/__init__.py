@@ -32,6 +32,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "LIB_PATH", "KQ_OK", "KQ_ERR_NULL", "KQ_ERR_SHAPE", "KQ_ERR_ALIGN", "KQ_ERR_CUDA", "KQ_ERR_VARIANT",
@@ -574,42 +575,37 @@ def mxf4_gemv(x, b_codes, b_sf, out=None, out_dtype=None, workspace=None, stream
     if b_codes.dim() != 2 or b_codes.shape[1] * 2 != K:
         raise ValueError(f"b_codes must be [N, {K // 2}], got {tuple(b_codes.shape)}")
     N = b_codes.shape[0]
-    _need(b_sf, "b_sf", torch.uint8, dev, (kq_sf_bytes(N, K),))
+    L = lib()
+    _need(b_sf, "b_sf", torch.uint8, dev, (L.kq_sf_bytes(N, K),))
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
-    if out.dtype not in (torch.bfloat16, torch.float32) or (out_dtype is not None and out.dtype != out_dtype):
+    else:
+        _need(out, "out", out.dtype, dev, (M, N))
+    f32 = out.dtype is torch.float32
+    if not (f32 or out.dtype is torch.bfloat16) or (out_dtype is not None and out.dtype != out_dtype):
         raise TypeError(f"out must be {out_dtype or 'bfloat16 or float32'}, got {out.dtype}")
-    _need(out, "out", out.dtype, dev, (M, N))
-    need = lib().mxf4_gemv_workspace(M, N, K)                # -1: sizes that the call refuses
-    if workspace is None and need > 0:
-        workspace = _scratch(need, dev, stream)
+    need = L.mxf4_gemv_workspace(M, N, K)                    # -1: sizes that the call refuses
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8, dev)
-    _call("mxf4_gemv", dev, _ptr(x), x.stride(0) if M > 1 else K, _ptr(b_codes), _ptr(b_sf), _ptr(out),
-          int(out.dtype == torch.float32), M, N, K, _ptr(workspace), 0 if workspace is None else workspace.numel(),
-          _stream(stream, dev))
+    elif need > 0:
+        workspace = _scratch(need, dev, stream)
+    _call("mxf4_gemv", dev, _ptr(x), x.stride(0) if M > 1 else K, _ptr(b_codes), _ptr(b_sf), _ptr(out), f32, M, N, K,
+          _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, dev))
     return out
 
 
-class _Cache(ctypes.Structure):
-    """mx_cache of the C header."""
-
-    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")] + \
-               [(n, ctypes.c_int64) for n in ("num_pages", "heads", "page_size", "head_dim")]
-
-
-class _Batch(ctypes.Structure):
-    """mx_batch of the C header."""
-
-    _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int64),
-                ("cu_seqlens", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("batch", ctypes.c_int64)]
-
+# mx_cache and mx_batch of the C header, passed as bytes.
+_CACHE = struct.Struct("4P4q")
+_BATCH = struct.Struct("PqqPPq")
 
 def _need_rows(t, name, dtypes, dim, device=None, shape=None):
     """An operand whose last dimension is contiguous and whose others may be strided."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype in dtypes and t.is_cuda and (device is None or t.device == device) and t.dim() == dim and \
+            (shape is None or t.shape == shape) and t.stride(-1) == 1:
+        return t
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if not t.is_cuda:
@@ -626,26 +622,32 @@ def _need_rows(t, name, dtypes, dim, device=None, shape=None):
 
 
 def _cache(k_codes, k_scales, v_codes, v_scales):
+    """(packed mx_cache, device, heads, head_dim) of a cache's four arrays."""
     torch = _torch()
     _need(k_codes, "k_codes", torch.uint8)
     if k_codes.dim() != 4:
         raise ValueError("k_codes must be [num_pages, heads, page_size, head_dim / 2]")
     dev = k_codes.device
-    P, H, S, half = k_codes.shape
-    _need(v_codes, "v_codes", torch.uint8, dev, (P, H, S, half))
-    _need(k_scales, "k_scales", torch.uint8, dev, (P, H, S, half // 16))
-    _need(v_scales, "v_scales", torch.uint8, dev, (P, H, S, half // 16))
-    return _Cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), P, H, S, 2 * half), dev
+    shape = k_codes.shape
+    P, H, S, half = shape
+    scales = (P, H, S, half // 16)
+    _need(v_codes, "v_codes", torch.uint8, dev, shape)
+    _need(k_scales, "k_scales", torch.uint8, dev, scales)
+    _need(v_scales, "v_scales", torch.uint8, dev, scales)
+    return _CACHE.pack(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), P, H, S, 2 * half), dev, H, 2 * half
 
 
 def _batch(block_table, cu_seqlens, seq_lens, device):
+    """(packed mx_batch, sequences) of a call's sequences."""
     torch = _torch()
     _need_rows(block_table, "block_table", (torch.int32,), 2, device)
     B, pages = block_table.shape
     _need(cu_seqlens, "cu_seqlens", torch.int32, device, (B + 1,))
+    lens = 0
     if seq_lens is not None:
         _need(seq_lens, "seq_lens", torch.int32, device, (B,))
-    return _Batch(_ptr(block_table), max(block_table.stride(0), pages), pages, _ptr(cu_seqlens), _ptr(seq_lens), B)
+        lens = _ptr(seq_lens)
+    return _BATCH.pack(_ptr(block_table), max(block_table.stride(0), pages), pages, _ptr(cu_seqlens), lens, B), B
 
 
 def mx_cache_write(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, seq_lens, stream=None):
@@ -658,16 +660,19 @@ def mx_cache_write(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_s
     seq_lens int32 [B] (lengths with the new tokens, which are the last ones).
     """
     torch = _torch()
-    c, dev = _cache(k_codes, k_scales, v_codes, v_scales)
-    b = _batch(block_table, cu_seqlens, seq_lens, dev)
+    c, dev, H, D = _cache(k_codes, k_scales, v_codes, v_scales)
+    b, _ = _batch(block_table, cu_seqlens, seq_lens, dev)
     if seq_lens is None:
         raise TypeError("seq_lens must be a torch.Tensor")
     _need_rows(k, "k", (torch.bfloat16, torch.float32), 3, dev)
-    if tuple(k.shape[1:]) != (c.heads, c.head_dim):
-        raise ValueError(f"k must be [T, {c.heads}, {c.head_dim}], got {tuple(k.shape)}")
-    _need_rows(v, "v", (k.dtype,), 3, dev, k.shape)
-    _call("mx_cache_write", dev, _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1),
-          int(k.dtype == torch.float32), ctypes.addressof(c), ctypes.addressof(b), k.shape[0], _stream(stream, dev))
+    shape = k.shape
+    T = shape[0]
+    if shape[1] != H or shape[2] != D:
+        raise ValueError(f"k must be [T, {H}, {D}], got {tuple(shape)}")
+    _need_rows(v, "v", (k.dtype,), 3, dev, shape)
+    kst, ksh, _ = k.stride()
+    vst, vsh, _ = v.stride()
+    _call("mx_cache_write", dev, _ptr(k), kst, ksh, _ptr(v), vst, vsh, k.dtype is torch.float32, c, b, T, _stream(stream, dev))
 
 
 def mx_cache_read(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, rows, starts=None, out_k=None,
@@ -678,20 +683,24 @@ def mx_cache_read(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens,
     (starts int32 [B], default zeros) of sequence b.
     """
     torch = _torch()
-    c, dev = _cache(k_codes, k_scales, v_codes, v_scales)
-    b = _batch(block_table, cu_seqlens, None, dev)
+    c, dev, H, D = _cache(k_codes, k_scales, v_codes, v_scales)
+    b, B = _batch(block_table, cu_seqlens, None, dev)
     if starts is not None:
-        _need(starts, "starts", torch.int32, dev, (b.batch,))
-    shape = (int(rows), c.heads, c.head_dim)
+        _need(starts, "starts", torch.int32, dev, (B,))
+    shape = (int(rows), H, D)
     dtype = out_dtype or (out_k.dtype if out_k is not None else torch.bfloat16)
-    if dtype not in (torch.bfloat16, torch.float32):
+    f32 = dtype is torch.float32
+    if not f32 and dtype is not torch.bfloat16:
         raise TypeError(f"out_k and out_v must be bfloat16 or float32, got {dtype}")
-    out_k = torch.empty(shape, dtype=dtype, device=dev) if out_k is None else out_k
-    out_v = torch.empty(shape, dtype=dtype, device=dev) if out_v is None else out_v
-    _need(out_k, "out_k", dtype, dev, shape)
-    _need(out_v, "out_v", dtype, dev, shape)
-    _call("mx_cache_read", dev, ctypes.addressof(c), ctypes.addressof(b), _ptr(starts), _ptr(out_k), _ptr(out_v),
-          int(dtype == torch.float32), shape[0], _stream(stream, dev))
+    if out_k is None:
+        out_k = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need(out_k, "out_k", dtype, dev, shape)
+    if out_v is None:
+        out_v = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need(out_v, "out_v", dtype, dev, shape)
+    _call("mx_cache_read", dev, c, b, _ptr(starts), _ptr(out_k), _ptr(out_v), f32, shape[0], _stream(stream, dev))
     return out_k, out_v
 
 
@@ -715,25 +724,29 @@ def mx_paged_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_
     tensor of mx_attention_workspace(...) bytes for this call alone; allocated if None.
     """
     torch = _torch()
-    c, dev = _cache(k_codes, k_scales, v_codes, v_scales)
-    b = _batch(block_table, cu_seqlens, seq_lens, dev)
+    c, dev, H, D = _cache(k_codes, k_scales, v_codes, v_scales)
+    b, _ = _batch(block_table, cu_seqlens, seq_lens, dev)
     if seq_lens is None:
         raise TypeError("seq_lens must be a torch.Tensor")
     _need_rows(q, "q", (torch.bfloat16,), 3, dev)
-    T, hq, d = q.shape
-    if d != c.head_dim or hq == 0 or c.heads == 0 or hq % c.heads:
-        raise ValueError(f"q must be [T, a multiple of {c.heads}, {c.head_dim}], got {tuple(q.shape)}")
+    T, hq, d = shape = q.shape
+    if d != D or hq == 0 or H == 0 or hq % H:
+        raise ValueError(f"q must be [T, a multiple of {H}, {D}], got {tuple(shape)}")
     max_new = T if max_new is None else int(max_new)
     scale = d ** -0.5 if scale is None else float(scale)
     if out is None:
-        out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
-    _need(out, "out", torch.bfloat16, dev, (T, hq, d))
-    need = mx_attention_workspace(T, hq, c.heads, d, max_new)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _need(out, "out", torch.bfloat16, dev, shape)
     if workspace is None:
+        need = mx_attention_workspace(T, hq, H, d, max_new)
         workspace = _scratch(need, dev, stream)
-    _need(workspace, "workspace", torch.uint8, dev)
-    _call("mx_paged_attention", dev, _ptr(q), q.stride(0), q.stride(1), ctypes.addressof(c), ctypes.addressof(b), scale,
-          int(bool(causal)), _ptr(out), T, hq, max_new, _ptr(workspace), workspace.numel(), _stream(stream, dev))
+    else:
+        _need(workspace, "workspace", torch.uint8, dev)
+        need = workspace.numel()
+    qst, qsh, _ = q.stride()
+    _call("mx_paged_attention", dev, _ptr(q), qst, qsh, c, b, scale, bool(causal), _ptr(out), T, hq, max_new,
+          _ptr(workspace), need, _stream(stream, dev))
     return out
 
 
