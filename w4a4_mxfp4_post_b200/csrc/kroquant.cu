@@ -2947,13 +2947,12 @@ int chunk_launch(const char *fn, const attn::Args &a, cudaStream_t stream)
     const int ctas = sms < attn::chunk::kMaxCtas ? sms : attn::chunk::kMaxCtas;
     launch(k, unsigned(ctas), attn::chunk::kThreads, C::kSmem, stream, a, kWaitBudget);
     if ((rc = launch_check(fn)) != KQ_OK) return rc;
-    constexpr int kPer = attn::chunk::R / attn::chunk::kMergeRows;
-    launch(attn::merge_kernel<attn::chunk::R, D, 256, attn::chunk::kMergeRows>, unsigned(ctas * kPer), 256, 0, stream, a);
+    launch(attn::chunk::merge_many_kernel<D>, unsigned(ctas * (D / 4 / attn::chunk::kMergeQuads)), 2 * attn::chunk::R, 0, stream, a);
     return launch_check(fn);
 }
 
 // Rows per kv head from which a sequence goes to the many-rows kernel.
-constexpr int64_t kChunkRows = 64;
+constexpr int64_t kChunkRows = 48;
 
 // max_new and T bound a sequence's rows; where there may be many, sequences
 // with more than kChunkRows go to the many-rows kernel (all of a single

@@ -45,15 +45,22 @@ struct Args {
 // What a CTA left behind: the item that its share ended in (rows > 0: split
 // there, `parts` shares hold it, this one the first).
 struct Desc {
-    int b, h, tile, parts;
+    int parts;
+    int h, r0;                               // kv head, first row
+    int lo, rows;                            // the sequence's first row of the call, its rows
+    int pad[3];
 };
 
-// Slot i of a workspace for R rows: unnormalised output [R][D], maxima [R], sums [R].
+// Slot i of a workspace for R rows: unnormalised output [D / 4][R][4] (a thread
+// per row writes whole lines), maxima [R], sums [R].
 template <int R, int D>
 __device__ __forceinline__ float *slot(const Args &a, int i)
 {
     return reinterpret_cast<float *>(a.work + kMaxCtas * sizeof(Desc)) + int64_t(i) * R * (D + 2);
 }
+
+template <int R>
+__device__ __forceinline__ int slot_at(int row, int d) { return ((d >> 2) * R + row) * 4 + (d & 3); }
 
 // A sequence as the kernels see it.
 struct Seq {
@@ -87,13 +94,15 @@ __device__ __forceinline__ int item_units(const Args &a, const Seq &q, int tile)
     return max(1, (row_end(a, q, min((tile + 1) * R, q.rows) - 1) + kUnit - 1) / kUnit);
 }
 
-template <int R>
-__device__ __forceinline__ int64_t head_units(const Args &a, const Seq &q)
+// What an item costs beside its units (queries, results, filling the pipeline)
+// counts as V units before its first: shares are cut in units and these.
+template <int R, int V>
+__device__ __forceinline__ int64_t head_cost(const Args &a, const Seq &q)
 {
     const int tiles = (q.rows + R - 1) / R;
-    if (!a.causal) return int64_t(tiles) * (tiles ? item_units<R>(a, q, 0) : 0);
+    if (!a.causal) return int64_t(tiles) * (tiles ? item_units<R>(a, q, 0) + V : 0);
     int64_t u = 0;
-    for (int t = 0; t < tiles; ++t) u += item_units<R>(a, q, t);
+    for (int t = 0; t < tiles; ++t) u += item_units<R>(a, q, t) + V;
     return u;
 }
 
@@ -102,66 +111,90 @@ struct Place {
     int b, h, tile, unit;
 };
 
-// The share of this CTA: its first unit's place and the number of units.  There
-// are `shares` of them, one for each CTA but no more than units, so that every
-// share between an item's first and last holds a part of it.  Every thread of
-// the CTA calls it; `sh` is shared memory of 34 int64.
-template <int R, int THREADS>
-__device__ __forceinline__ int64_t my_share(const Args &a, int64_t *sh, Place &p, int64_t &total, int64_t &first,
-                                            int &shares)
+// The share of this CTA: its first unit's place and its cost from there on (none
+// if it holds no unit).  There are `shares` of them, one for each CTA but no more
+// than units, so that every share between an item's first and last holds a part
+// of it.  Every thread of
+// the CTA calls it; `sh` is shared memory of THREADS + 34 int64.  The threads
+// count a head's units: of one sequence's tiles each (as many threads to a
+// sequence as there are), or of several sequences.
+template <int R, int V, int THREADS>
+__device__ __forceinline__ int64_t my_share(const Args &a, int64_t *sh, Place &p, int64_t &total, int &shares)
 {
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int per = (a.s.B + THREADS - 1) / THREADS;
-    const int b0 = min(tid * per, a.s.B), b1 = min(b0 + per, a.s.B);
+    const int split = a.s.B < THREADS ? THREADS / max(a.s.B, 1) : 1;         // threads of a sequence
+    const int per = (a.s.B + THREADS - 1) / THREADS;                         // or sequences of a thread
+    const int b0 = min(split > 1 ? tid / split : tid * per, a.s.B), b1 = split > 1 ? min(b0 + 1, a.s.B) : min(b0 + per, a.s.B);
+    auto first_tile = [&](int rows, int part) { return int(int64_t((rows + R - 1) / R) * part / split); };
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += head_units<R>(a, load_seq(a, b)) * a.s.heads;
+    for (int b = b0; b < b1; ++b) {
+        const Seq q = load_seq(a, b);
+        const int part = split > 1 ? tid % split : 0, t1 = first_tile(q.rows, part + 1);
+        int t = first_tile(q.rows, part);
+        if (a.causal)
+            for (; t < t1; ++t) mine += item_units<R>(a, q, t) + V;
+        else if (t < t1)
+            mine += int64_t(t1 - t) * (item_units<R>(a, q, t) + V);
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
         if (lane >= d) incl += v;
     }
-    if (lane == 31) sh[warp] = incl;
+    int64_t *sums = sh + THREADS;
+    if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    int64_t base = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) base += sh[w];
-        total += sh[w];
-    }
+    for (int w = 0; w < warp; ++w) incl += sums[w];
+    sh[tid] = incl;
+    __syncthreads();
+    total = sh[THREADS - 1] * a.s.heads;
     shares = int(min(int64_t(gridDim.x), total));
     if (int(blockIdx.x) >= shares) return 0;
-    first = total * blockIdx.x / shares;
+    const int64_t first = total * blockIdx.x / shares;
     const int64_t last = total * (blockIdx.x + 1) / shares;
-    int64_t at = base + incl - mine;         // units before this thread's sequences
-    int *place = reinterpret_cast<int *>(sh + 32);
-    if (first >= at && first < at + mine) {
-        int b = b0;
-        Seq q;
-        int64_t hu;
-        for (;; ++b) {                       // ends: the units of b0 .. b1 - 1 hold `first`
-            q = load_seq(a, b);
-            hu = head_units<R>(a, q);
-            if (first < at + hu * a.s.heads) break;
-            at += hu * a.s.heads;
-        }
+    int *place = reinterpret_cast<int *>(sums + 32);
+    const bool leads = b0 < b1 && (split == 1 || tid % split == 0);          // of its sequences' threads
+    int64_t at = (incl - mine) * a.s.heads;                                  // units before its sequences
+    if (leads && first >= at && first < sh[tid + split - 1] * a.s.heads) {
+        int b = b0, t = 0, h;
         int64_t off = first - at;
-        const int h = int(off / hu);
-        off -= h * hu;
-        int t = 0;
-        for (int u = item_units<R>(a, q, 0); off >= u; u = item_units<R>(a, q, ++t)) off -= u;
+        Seq q = load_seq(a, b);
+        if (split > 1) {
+            const int64_t before = incl - mine, hu = sh[tid + split - 1] - before;
+            h = int(off / hu);
+            off -= h * hu;
+            int lo = 0, hi = split - 1;      // the part that holds the unit
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (sh[tid + mid] - before > off) hi = mid;
+                else lo = mid + 1;
+            }
+            if (lo > 0) off -= sh[tid + lo - 1] - before;
+            t = first_tile(q.rows, lo);
+        } else {
+            int64_t hu = head_cost<R, V>(a, q);
+            while (off >= hu * a.s.heads) {  // ends: the units of b0 .. b1 - 1 hold `first`
+                off -= hu * a.s.heads;
+                q = load_seq(a, ++b);
+                hu = head_cost<R, V>(a, q);
+            }
+            h = int(off / hu);
+            off -= h * hu;
+        }
+        for (int u = item_units<R>(a, q, t) + V; off >= u; u = item_units<R>(a, q, ++t) + V) off -= u;
         place[0] = b;
         place[1] = h;
         place[2] = t;
         place[3] = int(off);
     }
     __syncthreads();
-    p = Place{place[0], place[1], place[2], place[3]};
-    return last - first;
+    // (a share that begins within the V begins with the first unit)
+    p = Place{place[0], place[1], place[2], max(place[3] - V, 0)};
+    return last - first - max(V - place[3], 0);
 }
 
-// The share that unit u is in: the last i with total * i / shares <= u.
+// The share that unit u is in (counted with the V): the last i with total * i / shares <= u.
 __device__ __forceinline__ int64_t share_of(int64_t u, int64_t total, int64_t shares)
 {
     return ((u + 1) * shares + total - 1) / total - 1;
@@ -244,6 +277,7 @@ struct Few {
     static constexpr int D = D_, NT = NT_;
     static constexpr int R = 8 * NT;
     static constexpr int kWarps = 4;
+    static constexpr int kItemCost = 1;                      // of an item beside its units, in units
     static constexpr int kMergeRows = 2;                     // rows that a CTA of the merge takes
     static constexpr int kStages = 3;
     static constexpr int NB = D / 32;
@@ -318,18 +352,17 @@ few_kernel(const Args a)
     pdl_wait();
     constexpr int D = C::D, NT = C::NT, R = C::R, NB = C::NB, MT = C::MT, W = C::kWarps, ST = C::kStages;
     extern __shared__ __align__(16) uint8_t smem_dyn[];
-    __shared__ int64_t sh[34];
+    __shared__ int64_t sh[W * 32 + 34];
     __shared__ int nan_first[4];             // per 32 channels: the first position of the item whose value is NaN
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
 
     Place p;
-    int64_t total, first;
+    int64_t total;
     int shares;
-    int64_t left = my_share<R, W * 32>(a, sh, p, total, first, shares);
+    int64_t left = my_share<R, C::kItemCost, W * 32>(a, sh, p, total, shares);
     Desc *desc = reinterpret_cast<Desc *>(a.work) + blockIdx.x;
-    if (threadIdx.x == 0) *desc = Desc{0, 0, 0, 0};
+    if (threadIdx.x == 0) desc->parts = 0;
     if (left <= 0) return;
-    int64_t at_unit = first;                 // among all units
 
     uint8_t *ring = smem_dyn + warp * C::kWarpBytes;
     float *ktab = reinterpret_cast<float *>(ring + ST * C::kStage);          // [32 positions][4]
@@ -756,7 +789,7 @@ few_kernel(const Args a)
                 *reinterpret_cast<uint32_t *>(a.out + (int64_t(q.lo + row / a.group) * a.hq + p.h * a.group + row % a.group) * D +
                                               d) = v;
             } else {
-                *reinterpret_cast<float2 *>(sl + r * D + d) = make_float2(x, y);
+                *reinterpret_cast<float2 *>(sl + slot_at<R>(r, d)) = make_float2(x, y);
                 if (d == 0) {
                     sl[R * D + r] = mm;
                     sl[R * D + R + r] = ll;
@@ -765,12 +798,11 @@ few_kernel(const Args a)
         }
         if (!whole && p.unit == 0 && threadIdx.x == 0) {
             // the item starts here and goes on: the shares up to the one with its last unit hold it
-            const int64_t last = at_unit + units - 1;
-            *desc = Desc{p.b, p.h, p.tile, int(share_of(last, total, shares)) - int(blockIdx.x) + 1};
+            const int64_t last = total * (blockIdx.x + 1) / shares - left + units - 1;
+            *desc = Desc{int(share_of(last, total, shares)) - int(blockIdx.x) + 1, p.h, r0, q.lo, q.rows, {}};
         }
         __syncthreads();
-        at_unit += count;
-        left -= count;
+        left -= count + C::kItemCost;
         if (left > 0) next_item<R>(a, q, p);
     }
 }
@@ -783,20 +815,33 @@ __global__ void __launch_bounds__(THREADS)
 merge_kernel(const Args a)
 {
     pdl_wait();
-    __shared__ float weight[ROWS][kMaxCtas];                 // of each part
+    __shared__ float weight[ROWS][kMaxCtas];                   // of each part
     __shared__ float sums[ROWS];
     const int share = int(blockIdx.x) / (R / ROWS), first = int(blockIdx.x) % (R / ROWS) * ROWS;
     const Desc d = reinterpret_cast<const Desc *>(a.work)[share];
     if (d.parts == 0) return;
-    const Seq q = load_seq(a, d.b);
-    const int r0 = d.tile * R + first, rows = min(ROWS, q.rows - r0);
+    const int r0 = d.r0 + first, rows = min(ROWS, d.rows - r0);
+    if (rows <= 0) return;
     auto part = [&](int k) { return slot<R, D>(a, k ? 2 * (share + k) : 2 * share + 1); };
+    // four channels of a row per thread, the parts dealt out to G groups of threads where there are more threads;
+    // the first two parts are on their way while the weights are found
+    constexpr int E = ROWS * D / 4, G = THREADS / E;
+    static_assert(G >= 1, "a thread for every four channels");
+    __shared__ float4 some[G][E];
+    const int e = threadIdx.x % E, grp = threadIdx.x / E, er = e % ROWS, ech = 4 * (e / ROWS);
+    const bool mine = grp < G && er < rows;
+    auto values = [&](int k) {
+        return mine && k < d.parts ? *reinterpret_cast<const float4 *>(part(k) + slot_at<R>(first + er, ech))
+                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    const float4 v0 = values(grp), v1 = values(grp + G);
     // a warp per row: the maximum, then every part's weight and the sum, lanes over the parts
     for (int r = threadIdx.x / 32; r < rows; r += THREADS / 32) {
         const int lane = threadIdx.x % 32;
-        float mm = -INFINITY;
+        float mm = -INFINITY, lk_first = 0.0f;
         for (int k = lane; k < d.parts; k += 32) {
             const float mk = part(k)[R * D + first + r];
+            lk_first = k == lane ? part(k)[R * D + R + first + r] : lk_first;
             weight[r][k] = mk;
             mm = fmaxf(mm, mk);
         }
@@ -804,7 +849,7 @@ merge_kernel(const Args a)
         for (int i = 16; i; i >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, i));
         float ll = 0.0f;
         for (int k = lane; k < d.parts; k += 32) {
-            const float mk = weight[r][k], lk = part(k)[R * D + R + first + r];
+            const float mk = weight[r][k], lk = k == lane ? lk_first : part(k)[R * D + R + first + r];
             // a part that saw nothing has nothing; a NaN sum reaches the result
             const float f = mk == -INFINITY ? (lk == 0.0f ? 0.0f : lk) : ex2(mk - mm);
             weight[r][k] = f;
@@ -815,40 +860,36 @@ merge_kernel(const Args a)
         if (lane == 0) sums[r] = ll;
     }
     __syncthreads();
-    // four channels of a row per thread, the parts dealt out to G groups of threads
-    constexpr int E = ROWS * D / 4, G = THREADS / E;
-    static_assert(G >= 1, "a thread for every four channels");
-    __shared__ float4 some[G][E];
-    const int e = threadIdx.x % E, grp = threadIdx.x / E, r = e / (D / 4), ch = 4 * (e % (D / 4));
-    if (grp < G && r < rows) {
+    if (mine) {
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int k = grp; k < d.parts; k += G) {
-            const float4 v = *reinterpret_cast<const float4 *>(part(k) + (first + r) * D + ch);
-            const float f = weight[r][k];
+        auto add = [&](const float4 v, float f) {
             x.x = fmaf(v.x, f, x.x);
             x.y = fmaf(v.y, f, x.y);
             x.z = fmaf(v.z, f, x.z);
             x.w = fmaf(v.w, f, x.w);
-        }
+        };
+        if (grp < d.parts) add(v0, weight[er][grp]);
+        if (grp + G < d.parts) add(v1, weight[er][grp + G]);
+#pragma unroll 8
+        for (int k = grp + 2 * G; k < d.parts; k += G) add(values(k), weight[er][k]);
         some[grp][e] = x;
     }
     __syncthreads();
-    if (threadIdx.x < E && r < rows) {
-        float4 x = some[0][e];
+    for (int i = threadIdx.x; i < rows * D / 4; i += THREADS) {              // by rows for the output
+        const int r = i / (D / 4), ch = i % (D / 4), row = r0 + r;
+        float4 x = some[0][ch * ROWS + r];
 #pragma unroll
-        for (int i = 1; i < G; ++i) {
-            const float4 v = some[i][e];
+        for (int k = 1; k < G; ++k) {
+            const float4 v = some[k][ch * ROWS + r];
             x.x += v.x;
             x.y += v.y;
             x.z += v.z;
             x.w += v.w;
         }
-        const int row = r0 + r;
         const float ll = sums[r], inv = 1.0f / ll;
         const uint2 v = ll == 0.0f && x.x == 0.0f ? make_uint2(0u, 0u)
                                                   : make_uint2(mma::pack_bf16x2(x.x * inv, x.y * inv), mma::pack_bf16x2(x.z * inv, x.w * inv));
-        *reinterpret_cast<uint2 *>(a.out + (int64_t(q.lo + row / a.group) * a.hq + d.h * a.group + row % a.group) * D + ch) = v;
+        *reinterpret_cast<uint2 *>(a.out + (int64_t(d.lo + row / a.group) * a.hq + d.h * a.group + row % a.group) * D + 4 * ch) = v;
     }
 }
 

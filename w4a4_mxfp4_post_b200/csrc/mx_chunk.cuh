@@ -55,7 +55,8 @@ constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;
 static_assert(kThreads == 512 && 256 * (kSoftmaxRegs + kOtherRegs) <= 512 * 128, "the split stays within the launch's registers");
 constexpr int kSegs = 2 * kRing;                             // segments whose NaN positions are kept
-constexpr int kMergeRows = 8;                                // rows that a CTA of the merge takes
+constexpr int kItemCost = 4;                                 // of an item beside its units, in units
+constexpr int kMergeQuads = 8;                               // channels / 4 that a CTA of the merge takes
 constexpr int kMaxCtas = 192;                                // shares
 constexpr float kSlack = 8.0f;                               // log2 of how far a maximum may be stale
 constexpr uint32_t kO = 256;                                 // tensor memory: S of tile i at 128 i, O at 256 + 128 i
@@ -243,7 +244,7 @@ chunk_kernel(const Args a, long long budget)
     pdl_wait();
     constexpr int D = C::D, NB = C::NB;
     extern __shared__ __align__(16) uint8_t smem_dyn[];
-    __shared__ int64_t sh[34];
+    __shared__ int64_t sh[kThreads + 34];
     __shared__ uint32_t tmem_slot;
     __shared__ uint32_t visible[4][4];       // of step s % 4: the positions that are on a page, 32 to a word
     __shared__ int nan_first[kSegs][4];      // of segment i % kSegs, per 32 channels: the first position whose value is NaN
@@ -279,11 +280,11 @@ chunk_kernel(const Args a, long long budget)
     __shared__ int64_t totals[2];            // units of all shares, shares
     {
         Place p;
-        int64_t total, first;
+        int64_t total;
         int shares;
-        const int64_t left = my_share<R, kThreads>(a, sh, p, total, first, shares);
+        const int64_t left = my_share<R, kItemCost, kThreads>(a, sh, p, total, shares);
         if (tid == 0) {
-            reinterpret_cast<Desc *>(a.work)[blockIdx.x] = Desc{0, 0, 0, 0};
+            reinterpret_cast<Desc *>(a.work)[blockIdx.x].parts = 0;
             totals[0] = total;
             totals[1] = shares;
         }
@@ -323,7 +324,7 @@ chunk_kernel(const Args a, long long budget)
     auto advance = [&] {
         __syncwarp();
         if (lane == 0) {
-            walk.left -= walk.count;
+            walk.left -= walk.count + kItemCost;
             if (walk.left > 0) {
                 Place p = walk.p;
                 Seq q = walk.q;
@@ -473,6 +474,7 @@ chunk_kernel(const Args a, long long budget)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int i = warp / 4, row = tid % kTile;
         const uint32_t lanes = uint32_t(warp % 4) << 21;                     // 32 (warp % 4) in the lane field
+        uint8_t *tile_q = sQ + i * C::kQBytes;
         const uint32_t tS = tmem + lanes + i * 128, tO = tmem + lanes + kO + i * 128;
         int n = 0;                           // steps of this tile so far
         int k = 0;                           // steps so far
@@ -501,22 +503,24 @@ chunk_kernel(const Args a, long long budget)
                 {
                     const Seq q = walk.q;
                     const int r = r0 + row, token = r / a.group, head = walk.p.h * a.group + r - token * a.group;
-                    const bool mine = r < q.rows;
-                    lim = mine ? row_end(a, q, r) - walk.t_first : 0x7fffffff;
-                    const __nv_bfloat16 *src = a.q + int64_t(q.lo + token) * a.q_st + int64_t(head) * a.q_sh;
-                    uint8_t *dst = sQ + i * C::kQBytes + row * 128;
+                    lim = r < q.rows ? row_end(a, q, r) - walk.t_first : 0x7fffffff;
+                    const int64_t from = int64_t(q.lo + token) * a.q_st + int64_t(head) * a.q_sh;
                     const uint32_t sgn = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-#pragma unroll
-                    for (int ch = 0; ch < D / 8; ++ch) {
+                    // lanes over the chunks of the warp's rows, so that every load is contiguous
+#pragma unroll 8
+                    for (int e = 0; e < D / 8; ++e) {
+                        const int pc = lane + 32 * e, rr = pc / (D / 8), ch = pc % (D / 8);
+                        const int64_t at = __shfl_sync(0xffffffffu, from, rr);
+                        const int rw = row - lane + rr;
                         uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                        if (mine) w = __ldg(reinterpret_cast<const uint4 *>(src) + ch);
+                        if (r0 + rw < q.rows) w = __ldg(reinterpret_cast<const uint4 *>(a.q + at) + ch);
                         if (a.scale_log2 == 0.0f) {
                             w.x = hmul2_bf16(w.x, 0u);
                             w.y = hmul2_bf16(w.y, 0u);
                             w.z = hmul2_bf16(w.z, 0u);
                             w.w = hmul2_bf16(w.w, 0u);
                         }
-                        *reinterpret_cast<uint4 *>(dst + (ch / 8) * (kTile * 128) + (((ch % 8) ^ (row & 7)) << 4)) =
+                        *reinterpret_cast<uint4 *>(tile_q + rw * 128 + (ch / 8) * (kTile * 128) + (((ch % 8) ^ (rw & 7)) << 4)) =
                             make_uint4(__byte_perm(w.x, w.z, 0x5410) ^ sgn, __byte_perm(w.x, w.z, 0x7632) ^ sgn,
                                        __byte_perm(w.y, w.w, 0x5410) ^ sgn, __byte_perm(w.y, w.w, 0x7632) ^ sgn);
                     }
@@ -633,7 +637,6 @@ chunk_kernel(const Args a, long long budget)
                 const bool whole = walk.count == units;
                 float *sl = slot<R, D>(a, 2 * int(blockIdx.x) + (p.unit == 0 ? 1 : 0));
                 const int ir = i * kTile + row;                              // row of the item
-                const int token = r / a.group, head = p.h * a.group + r - token * a.group;
                 const float inv = 1.0f / l;
                 if (!whole && mine) {
                     sl[R * D + ir] = m == -INFINITY ? m : m * c;
@@ -645,36 +648,47 @@ chunk_kernel(const Args a, long long budget)
                     tmem_ld16(tO + 16 * j, o);
                     tmem_wait_ld();
                     const bool nan = nan_first[seg % kSegs][j / 2] < sees;
-                    if (mine) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            // columns hold channels 0 4 1 5 2 6 3 7
-                            float v[8] = {o[8 * h], o[8 * h + 2], o[8 * h + 4], o[8 * h + 6],
-                                          o[8 * h + 1], o[8 * h + 3], o[8 * h + 5], o[8 * h + 7]};
+                    for (int h = 0; h < 2; ++h) {
+                        // columns hold channels 0 4 1 5 2 6 3 7
+                        float v[8] = {o[8 * h], o[8 * h + 2], o[8 * h + 4], o[8 * h + 6],
+                                      o[8 * h + 1], o[8 * h + 3], o[8 * h + 5], o[8 * h + 7]};
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                if (nan) v[e] = __uint_as_float(0x7fc00000u);
-                                if (whole) v[e] = l == 0.0f && v[e] == 0.0f ? 0.0f : v[e] * inv;
-                            }
-                            const int ch = 16 * j + 8 * h;
-                            if (whole) {
-                                *reinterpret_cast<uint4 *>(a.out + (int64_t(q.lo + token) * a.hq + head) * D + ch) =
-                                    make_uint4(mma::pack_bf16x2(v[0], v[1]), mma::pack_bf16x2(v[2], v[3]),
-                                               mma::pack_bf16x2(v[4], v[5]), mma::pack_bf16x2(v[6], v[7]));
-                            } else {
-                                float *dst = sl + int64_t(ir) * D + ch;
-                                *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-                                *reinterpret_cast<float4 *>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
-                            }
+                        for (int e = 0; e < 8; ++e) {
+                            if (nan) v[e] = __uint_as_float(0x7fc00000u);
+                            if (whole) v[e] = l == 0.0f && v[e] == 0.0f ? 0.0f : v[e] * inv;
+                        }
+                        const int ch = 2 * j + h;                            // of 8 channels
+                        if (whole) {
+                            // by way of Q's place, which the segment has done with, so that rows are written whole
+                            *reinterpret_cast<uint4 *>(tile_q + row * 128 + (ch / 8) * (kTile * 128) + (((ch % 8) ^ (row & 7)) << 4)) =
+                                make_uint4(mma::pack_bf16x2(v[0], v[1]), mma::pack_bf16x2(v[2], v[3]),
+                                           mma::pack_bf16x2(v[4], v[5]), mma::pack_bf16x2(v[6], v[7]));
+                        } else if (mine) {
+                            *reinterpret_cast<float4 *>(sl + slot_at<R>(ir, 8 * ch)) = make_float4(v[0], v[1], v[2], v[3]);
+                            *reinterpret_cast<float4 *>(sl + slot_at<R>(ir, 8 * ch + 4)) = make_float4(v[4], v[5], v[6], v[7]);
                         }
                     }
+                }
+                __syncwarp();
+                if (whole) {
+                    const int token = r / a.group;
+                    const int64_t to = (int64_t(q.lo + token) * a.hq + p.h * a.group + r - token * a.group) * D;
+#pragma unroll 4
+                    for (int e = 0; e < D / 8; ++e) {
+                        const int pc = lane + 32 * e, rr = pc / (D / 8), ch = pc % (D / 8), rw = row - lane + rr;
+                        const int64_t at = __shfl_sync(0xffffffffu, to, rr);
+                        const uint4 w = *reinterpret_cast<const uint4 *>(tile_q + rw * 128 + (ch / 8) * (kTile * 128) + (((ch % 8) ^ (rw & 7)) << 4));
+                        if (r0 + rw < q.rows) *reinterpret_cast<uint4 *>(a.out + at + 8 * ch) = w;
+                    }
+                    __syncwarp();
                 }
                 mma::tc_fence_before();
                 if (tid == 0 && !whole && p.unit == 0) {
                     const int64_t total = totals[0], shares = totals[1];
                     const int64_t end = total * (blockIdx.x + 1) / shares - walk.left + units - 1;
                     reinterpret_cast<Desc *>(a.work)[blockIdx.x] =
-                        Desc{p.b, p.h, p.tile, int(share_of(end, total, shares)) - int(blockIdx.x) + 1};
+                        Desc{int(share_of(end, total, shares)) - int(blockIdx.x) + 1, p.h, p.tile * R, q.lo, q.rows, {}};
                 }
             }
             k += steps;
@@ -687,6 +701,61 @@ chunk_kernel(const Args a, long long budget)
     if (warp == kMmaWarp) {
         mma::tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// The items that were split, as in merge_kernel, for many rows and (mostly) two
+// parts: a thread per row and 16 channels, which finds its row's weights itself
+// and has the first two parts' values on their way meanwhile.
+template <int D>
+__global__ void __launch_bounds__(2 * R)
+merge_many_kernel(const Args a)
+{
+    pdl_wait();
+    constexpr int kPer = kMergeQuads / 2;                    // quads of a thread
+    const int share = int(blockIdx.x) / (D / 4 / kMergeQuads), r = threadIdx.x % R;
+    const int quad = int(blockIdx.x) % (D / 4 / kMergeQuads) * kMergeQuads + int(threadIdx.x) / R * kPer;
+    const Desc d = reinterpret_cast<const Desc *>(a.work)[share];
+    if (d.parts == 0 || d.r0 + r >= d.rows) return;
+    auto part = [&](int k) { return slot<R, D>(a, k ? 2 * (share + k) : 2 * share + 1); };
+    auto load = [&](float4 (&v)[kPer], int k) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[j] = *reinterpret_cast<const float4 *>(part(k) + slot_at<R>(r, 4 * (quad + j)));
+    };
+    float4 v0[kPer], v1[kPer];
+    load(v0, 0);                                             // (two parts at least)
+    load(v1, 1);
+    float mm = -INFINITY, ll = 0.0f;
+    for (int k = 0; k < d.parts; ++k) mm = fmaxf(mm, part(k)[R * D + r]);
+    float4 x[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = 0; k < d.parts; ++k) {
+        const float mk = part(k)[R * D + r], lk = part(k)[R * D + R + r];
+        // a part that saw nothing has nothing; a NaN sum reaches the result
+        const float f = mk == -INFINITY ? (lk == 0.0f ? 0.0f : lk) : ex2(mk - mm);
+        ll = fmaf(lk, f, ll);
+        float4 v[kPer];
+        if (k > 1) load(v, k);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const float4 u = k == 0 ? v0[j] : k == 1 ? v1[j] : v[j];
+            x[j].x = fmaf(u.x, f, x[j].x);
+            x[j].y = fmaf(u.y, f, x[j].y);
+            x[j].z = fmaf(u.z, f, x[j].z);
+            x[j].w = fmaf(u.w, f, x[j].w);
+        }
+    }
+    const float inv = 1.0f / ll;
+    const int row = d.r0 + r, token = row / a.group;
+    __nv_bfloat16 *out = a.out + (int64_t(d.lo + token) * a.hq + d.h * a.group + row - token * a.group) * D + 4 * quad;
+#pragma unroll
+    for (int j = 0; j < kPer; j += 2) {
+        auto pair = [&](float u, float w) {
+            return mma::pack_bf16x2(ll == 0.0f && u == 0.0f ? 0.0f : u * inv, ll == 0.0f && w == 0.0f ? 0.0f : w * inv);
+        };
+        *reinterpret_cast<uint4 *>(out + 4 * j) = make_uint4(pair(x[j].x, x[j].y), pair(x[j].z, x[j].w),
+                                                             pair(x[j + 1].x, x[j + 1].y), pair(x[j + 1].z, x[j + 1].w));
     }
 }
 
