@@ -106,6 +106,13 @@ __device__ __forceinline__ int64_t head_cost(const Args &a, const Seq &q)
     return u;
 }
 
+// x / y of numbers that are not negative: in 32 bits where they are that small,
+// for a division of 64 takes hundreds of clocks.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y)
+{
+    return ((x | y) >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : x / y;
+}
+
 // A place in the order of units: sequence, head, tile, unit of the item.
 struct Place {
     int b, h, tile, unit;
@@ -125,7 +132,10 @@ __device__ __forceinline__ int64_t my_share(const Args &a, int64_t *sh, Place &p
     const int split = a.s.B < THREADS ? THREADS / max(a.s.B, 1) : 1;         // threads of a sequence
     const int per = (a.s.B + THREADS - 1) / THREADS;                         // or sequences of a thread
     const int b0 = min(split > 1 ? tid / split : tid * per, a.s.B), b1 = split > 1 ? min(b0 + 1, a.s.B) : min(b0 + per, a.s.B);
-    auto first_tile = [&](int rows, int part) { return int(int64_t((rows + R - 1) / R) * part / split); };
+    auto first_tile = [&](int rows, int part) {
+        const int tiles = (rows + R - 1) / R, each = tiles / split;
+        return part * each + min(part, tiles - each * split);
+    };
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) {
         const Seq q = load_seq(a, b);
@@ -151,8 +161,8 @@ __device__ __forceinline__ int64_t my_share(const Args &a, int64_t *sh, Place &p
     total = sh[THREADS - 1] * a.s.heads;
     shares = int(min(int64_t(gridDim.x), total));
     if (int(blockIdx.x) >= shares) return 0;
-    const int64_t first = total * blockIdx.x / shares;
-    const int64_t last = total * (blockIdx.x + 1) / shares;
+    const int64_t first = quotient(total * blockIdx.x, shares);
+    const int64_t last = quotient(total * (blockIdx.x + 1), shares);
     int *place = reinterpret_cast<int *>(sums + 32);
     const bool leads = b0 < b1 && (split == 1 || tid % split == 0);          // of its sequences' threads
     int64_t at = (incl - mine) * a.s.heads;                                  // units before its sequences
@@ -162,7 +172,7 @@ __device__ __forceinline__ int64_t my_share(const Args &a, int64_t *sh, Place &p
         Seq q = load_seq(a, b);
         if (split > 1) {
             const int64_t before = incl - mine, hu = sh[tid + split - 1] - before;
-            h = int(off / hu);
+            h = int(quotient(off, hu));
             off -= h * hu;
             int lo = 0, hi = split - 1;      // the part that holds the unit
             while (lo < hi) {
@@ -179,7 +189,7 @@ __device__ __forceinline__ int64_t my_share(const Args &a, int64_t *sh, Place &p
                 q = load_seq(a, ++b);
                 hu = head_cost<R, V>(a, q);
             }
-            h = int(off / hu);
+            h = int(quotient(off, hu));
             off -= h * hu;
         }
         for (int u = item_units<R>(a, q, t) + V; off >= u; u = item_units<R>(a, q, ++t) + V) off -= u;
@@ -197,7 +207,7 @@ __device__ __forceinline__ int64_t my_share(const Args &a, int64_t *sh, Place &p
 // The share that unit u is in (counted with the V): the last i with total * i / shares <= u.
 __device__ __forceinline__ int64_t share_of(int64_t u, int64_t total, int64_t shares)
 {
-    return ((u + 1) * shares + total - 1) / total - 1;
+    return quotient((u + 1) * shares + total - 1, total) - 1;
 }
 
 // The next item after (b, h, tile): tiles, then heads, then sequences that have rows.
@@ -798,7 +808,7 @@ few_kernel(const Args a)
         }
         if (!whole && p.unit == 0 && threadIdx.x == 0) {
             // the item starts here and goes on: the shares up to the one with its last unit hold it
-            const int64_t last = total * (blockIdx.x + 1) / shares - left + units - 1;
+            const int64_t last = quotient(total * (blockIdx.x + 1), shares) - left + units - 1;
             *desc = Desc{int(share_of(last, total, shares)) - int(blockIdx.x) + 1, p.h, r0, q.lo, q.rows, {}};
         }
         __syncthreads();

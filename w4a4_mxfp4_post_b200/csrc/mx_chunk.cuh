@@ -686,7 +686,7 @@ chunk_kernel(const Args a, long long budget)
                 mma::tc_fence_before();
                 if (tid == 0 && !whole && p.unit == 0) {
                     const int64_t total = totals[0], shares = totals[1];
-                    const int64_t end = total * (blockIdx.x + 1) / shares - walk.left + units - 1;
+                    const int64_t end = quotient(total * (blockIdx.x + 1), shares) - walk.left + units - 1;
                     reinterpret_cast<Desc *>(a.work)[blockIdx.x] =
                         Desc{int(share_of(end, total, shares)) - int(blockIdx.x) + 1, p.h, p.tile * R, q.lo, q.rows, {}};
                 }
