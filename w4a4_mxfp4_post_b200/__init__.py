@@ -31,6 +31,7 @@ A few tokens at a time (a 4-bit layer that answers):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -177,6 +178,12 @@ def _stream(stream, device):
 
 def _ptr(t) -> int:
     return t.data_ptr() if t is not None and t.numel() > 0 else 0
+
+
+@functools.lru_cache(maxsize=1024)
+def _sizes(name, *args) -> int:
+    """What a size query of the library says (a function of its arguments alone)."""
+    return getattr(lib(), name)(*args)
 
 
 def _need(t, name, dtype, device=None, shape=None):
@@ -554,7 +561,7 @@ def norm_kq_quantize_sf(h, gamma, beta, factors, eps=1e-6, shared=False, out_cod
 
 def mxf4_gemv_workspace(M: int, N: int, K: int) -> int:
     """Bytes of workspace that mxf4_gemv needs for calls of these sizes."""
-    n = lib().mxf4_gemv_workspace(int(M), int(N), int(K))
+    n = _sizes("mxf4_gemv_workspace", int(M), int(N), int(K))
     if n < 0:
         raise ValueError(f"mxf4_gemv_workspace: bad sizes {M}, {N}, {K}")
     return n
@@ -568,30 +575,49 @@ def mxf4_gemv(x, b_codes, b_sf, out=None, out_dtype=None, workspace=None, stream
     tensor of mxf4_gemv_workspace(M, N, K) bytes for this call alone; allocated if None.
     """
     torch = _torch()
-    _need_rows(x, "x", (torch.bfloat16,), 2)
-    M, K = x.shape
+    u8 = torch.uint8
+    M, N = _gemv_sizes(x, b_codes, b_sf)
+    K = x.shape[1]
     dev = x.device
-    _need(b_codes, "b_codes", torch.uint8, dev)
-    if b_codes.dim() != 2 or b_codes.shape[1] * 2 != K:
-        raise ValueError(f"b_codes must be [N, {K // 2}], got {tuple(b_codes.shape)}")
-    N = b_codes.shape[0]
-    L = lib()
-    _need(b_sf, "b_sf", torch.uint8, dev, (L.kq_sf_bytes(N, K),))
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
+        out = x.new_empty((M, N), dtype=out_dtype)
     else:
         _need(out, "out", out.dtype, dev, (M, N))
     f32 = out.dtype is torch.float32
     if not (f32 or out.dtype is torch.bfloat16) or (out_dtype is not None and out.dtype != out_dtype):
         raise TypeError(f"out must be {out_dtype or 'bfloat16 or float32'}, got {out.dtype}")
-    need = L.mxf4_gemv_workspace(M, N, K)                    # -1: sizes that the call refuses
+    need = _sizes("mxf4_gemv_workspace", M, N, K)            # -1: sizes that the call refuses
     if workspace is not None:
-        _need(workspace, "workspace", torch.uint8, dev)
+        _need(workspace, "workspace", u8, dev)
     elif need > 0:
         workspace = _scratch(need, dev, stream)
-    _call("mxf4_gemv", dev, _ptr(x), x.stride(0) if M > 1 else K, _ptr(b_codes), _ptr(b_sf), _ptr(out), f32, M, N, K,
+    _call("mxf4_gemv", dev, x.data_ptr(), x.stride(0) if M > 1 else K, b_codes.data_ptr(), b_sf.data_ptr(), out.data_ptr(),
+          f32, M, N, K,
           _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, dev))
     return out
+
+
+def _gemv_sizes(x, b_codes, b_sf):
+    """M and N of mxf4_gemv's operands, checked (as in _cache: at once, and one by one to say what is wrong)."""
+    torch = _torch()
+    u8 = torch.uint8
+    try:
+        M, K = x.shape
+        N, half = b_codes.shape
+        dev = x.device
+        if x.dtype is torch.bfloat16 and b_codes.dtype is u8 and b_sf.dtype is u8 and x.is_cuda and b_codes.device == dev \
+                and b_sf.device == dev and 2 * half == K and x.stride(1) == 1 and b_codes.is_contiguous() \
+                and b_sf.shape == (_sizes("kq_sf_bytes", N, K),) and b_sf.is_contiguous():
+            return M, N
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _need_rows(x, "x", (torch.bfloat16,), 2)
+    M, K = x.shape
+    _need(b_codes, "b_codes", u8, x.device)
+    if b_codes.dim() != 2 or b_codes.shape[1] * 2 != K:
+        raise ValueError(f"b_codes must be [N, {K // 2}], got {tuple(b_codes.shape)}")
+    _need(b_sf, "b_sf", u8, x.device, (kq_sf_bytes(b_codes.shape[0], K),))
+    return M, b_codes.shape[0]
 
 
 # mx_cache and mx_batch of the C header, passed as bytes.
@@ -624,30 +650,51 @@ def _need_rows(t, name, dtypes, dim, device=None, shape=None):
 def _cache(k_codes, k_scales, v_codes, v_scales):
     """(packed mx_cache, device, heads, head_dim) of a cache's four arrays."""
     torch = _torch()
-    _need(k_codes, "k_codes", torch.uint8)
+    u8 = torch.uint8
+    try:
+        # these calls are made once per layer and token: all of it at once, and one by one only to say what is wrong
+        shape = k_codes.shape
+        P, H, S, half = shape
+        scales = (P, H, S, half // 16)
+        dev = k_codes.device
+        if k_codes.dtype is u8 and v_codes.dtype is u8 and k_scales.dtype is u8 and v_scales.dtype is u8 and k_codes.is_cuda \
+                and v_codes.device == dev and k_scales.device == dev and v_scales.device == dev \
+                and v_codes.shape == shape and k_scales.shape == scales and v_scales.shape == scales \
+                and k_codes.is_contiguous() and v_codes.is_contiguous() and k_scales.is_contiguous() and v_scales.is_contiguous():
+            return _CACHE.pack(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), P, H, S,
+                               2 * half), dev, H, 2 * half
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _need(k_codes, "k_codes", u8)
     if k_codes.dim() != 4:
         raise ValueError("k_codes must be [num_pages, heads, page_size, head_dim / 2]")
-    dev = k_codes.device
-    shape = k_codes.shape
-    P, H, S, half = shape
-    scales = (P, H, S, half // 16)
-    _need(v_codes, "v_codes", torch.uint8, dev, shape)
-    _need(k_scales, "k_scales", torch.uint8, dev, scales)
-    _need(v_scales, "v_scales", torch.uint8, dev, scales)
-    return _CACHE.pack(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), P, H, S, 2 * half), dev, H, 2 * half
+    _need(v_codes, "v_codes", u8, dev, shape)
+    _need(k_scales, "k_scales", u8, dev, scales)
+    _need(v_scales, "v_scales", u8, dev, scales)
+    raise ValueError("the cache's arrays do not fit together")
 
 
 def _batch(block_table, cu_seqlens, seq_lens, device):
-    """(packed mx_batch, sequences) of a call's sequences."""
-    torch = _torch()
-    _need_rows(block_table, "block_table", (torch.int32,), 2, device)
-    B, pages = block_table.shape
-    _need(cu_seqlens, "cu_seqlens", torch.int32, device, (B + 1,))
-    lens = 0
-    if seq_lens is not None:
-        _need(seq_lens, "seq_lens", torch.int32, device, (B,))
-        lens = _ptr(seq_lens)
-    return _BATCH.pack(_ptr(block_table), max(block_table.stride(0), pages), pages, _ptr(cu_seqlens), lens, B), B
+    """(packed mx_batch, sequences) of a call's sequences; seq_lens None where the call reads none."""
+    i32 = _torch().int32
+    try:
+        B, pages = block_table.shape
+        stride, inner = block_table.stride()
+        if block_table.dtype is i32 and cu_seqlens.dtype is i32 and block_table.device == device \
+                and cu_seqlens.device == device and (inner == 1 or pages <= 1) and cu_seqlens.shape == (B + 1,) \
+                and cu_seqlens.is_contiguous():
+            if seq_lens is None:
+                return _BATCH.pack(block_table.data_ptr(), max(stride, pages), pages, cu_seqlens.data_ptr(), 0, B), B
+            if seq_lens.dtype is i32 and seq_lens.device == device and seq_lens.shape == (B,) and seq_lens.is_contiguous():
+                return _BATCH.pack(block_table.data_ptr(), max(stride, pages), pages, cu_seqlens.data_ptr(),
+                                   seq_lens.data_ptr(), B), B
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _need_rows(block_table, "block_table", (i32,), 2, device)
+    B = block_table.shape[0]
+    _need(cu_seqlens, "cu_seqlens", i32, device, (B + 1,))
+    _need(seq_lens, "seq_lens", i32, device, (B,))
+    raise ValueError("block_table, cu_seqlens and seq_lens do not fit together")
 
 
 def mx_cache_write(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, seq_lens, stream=None):
@@ -661,9 +708,9 @@ def mx_cache_write(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_s
     """
     torch = _torch()
     c, dev, H, D = _cache(k_codes, k_scales, v_codes, v_scales)
-    b, _ = _batch(block_table, cu_seqlens, seq_lens, dev)
     if seq_lens is None:
         raise TypeError("seq_lens must be a torch.Tensor")
+    b, _ = _batch(block_table, cu_seqlens, seq_lens, dev)
     _need_rows(k, "k", (torch.bfloat16, torch.float32), 3, dev)
     shape = k.shape
     T = shape[0]
@@ -672,7 +719,7 @@ def mx_cache_write(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_s
     _need_rows(v, "v", (k.dtype,), 3, dev, shape)
     kst, ksh, _ = k.stride()
     vst, vsh, _ = v.stride()
-    _call("mx_cache_write", dev, _ptr(k), kst, ksh, _ptr(v), vst, vsh, k.dtype is torch.float32, c, b, T, _stream(stream, dev))
+    _call("mx_cache_write", dev, k.data_ptr(), kst, ksh, v.data_ptr(), vst, vsh, k.dtype is torch.float32, c, b, T, _stream(stream, dev))
 
 
 def mx_cache_read(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, rows, starts=None, out_k=None,
@@ -693,20 +740,20 @@ def mx_cache_read(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens,
     if not f32 and dtype is not torch.bfloat16:
         raise TypeError(f"out_k and out_v must be bfloat16 or float32, got {dtype}")
     if out_k is None:
-        out_k = torch.empty(shape, dtype=dtype, device=dev)
+        out_k = k_codes.new_empty(shape, dtype=dtype)
     else:
         _need(out_k, "out_k", dtype, dev, shape)
     if out_v is None:
-        out_v = torch.empty(shape, dtype=dtype, device=dev)
+        out_v = torch.empty_like(out_k)
     else:
         _need(out_v, "out_v", dtype, dev, shape)
-    _call("mx_cache_read", dev, c, b, _ptr(starts), _ptr(out_k), _ptr(out_v), f32, shape[0], _stream(stream, dev))
+    _call("mx_cache_read", dev, c, b, _ptr(starts), out_k.data_ptr(), out_v.data_ptr(), f32, shape[0], _stream(stream, dev))
     return out_k, out_v
 
 
 def mx_attention_workspace(rows: int, heads_q: int, heads: int, head_dim: int, max_new: int) -> int:
     """Bytes of workspace that mx_paged_attention needs for calls of these sizes."""
-    n = lib().mx_attention_workspace(int(rows), int(heads_q), int(heads), int(head_dim), int(max_new))
+    n = _sizes("mx_attention_workspace", int(rows), int(heads_q), int(heads), int(head_dim), int(max_new))
     if n < 0:
         raise ValueError(f"mx_attention_workspace: bad sizes {rows}, {heads_q}, {heads}, {head_dim}, {max_new}")
     return n
@@ -725,9 +772,9 @@ def mx_paged_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_
     """
     torch = _torch()
     c, dev, H, D = _cache(k_codes, k_scales, v_codes, v_scales)
-    b, _ = _batch(block_table, cu_seqlens, seq_lens, dev)
     if seq_lens is None:
         raise TypeError("seq_lens must be a torch.Tensor")
+    b, _ = _batch(block_table, cu_seqlens, seq_lens, dev)
     _need_rows(q, "q", (torch.bfloat16,), 3, dev)
     T, hq, d = shape = q.shape
     if d != D or hq == 0 or H == 0 or hq % H:
@@ -745,8 +792,8 @@ def mx_paged_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_
         _need(workspace, "workspace", torch.uint8, dev)
         need = workspace.numel()
     qst, qsh, _ = q.stride()
-    _call("mx_paged_attention", dev, _ptr(q), qst, qsh, c, b, scale, bool(causal), _ptr(out), T, hq, max_new,
-          _ptr(workspace), need, _stream(stream, dev))
+    _call("mx_paged_attention", dev, q.data_ptr(), qst, qsh, c, b, scale, bool(causal), out.data_ptr(), T, hq, max_new,
+          workspace.data_ptr(), need, _stream(stream, dev))
     return out
 
 
