@@ -45,8 +45,8 @@ def test_gemv_refusals(L):
     assert call(x=8) == -3 and call(c=8) == -3 and call(s=4) == -3 and call(o=8) == -3 and call(ldx=68) == -3
     assert call(x=None, c=None, s=None, o=None, M=0) == 0 and call(x=None, c=None, s=None, o=None, N=0) == 0
     assert err(L) == ""
-    big = dict(M=9, N=1 << 20, K=1 << 12, ldx=1 << 12)
-    need = L.mxf4_gemv_workspace(9, 1 << 20, 1 << 12)
+    big = dict(M=17, N=1 << 20, K=1 << 12, ldx=1 << 12)
+    need = L.mxf4_gemv_workspace(17, 1 << 20, 1 << 12)
     assert need > 0 and L.mxf4_gemv_workspace(2, 8, 64) == 0 and L.mxf4_gemv_workspace(0, 1 << 20, 1 << 12) == 0
     assert call(**big, ws=16, n=need - 1) == -2 and "workspace" in err(L)
     assert call(**big, n=need) == -1 and call(**big, ws=8, n=need) == -3

@@ -2790,11 +2790,13 @@ struct GemvArgs {
 };
 
 // Whether x is converted by a kernel of its own.  Measured, us with and without
-// (GPU time): 16 x 1152 x 1152 6.5 / 8.5, 32 x 8192 x 28672 88 / 180, 8 x 4096 x
-// 4096 8.5 / 11.1, 8 x 1152 x 1152 5.5 / 4.9, 1 x 8192 x 28672 38.5 / 34.3: with
-// more than 8 rows always, with more than 4 from kGemvPre pieces of 128 weight
-// rows x 256 channels.
-constexpr int64_t kGemvPre = 256;
+// (GPU time): 32 x 1152 x 1152 8.2 / 10.9, 32 x 4096 x 4096 13.4 / 30, 16 x 8192 x
+// 28672 51 / 63, 16 x 4096 x 4096 10.4 / 12.0, 8 x 8192 x 28672 37 / 43, 8 x 4096 x
+// 4096 9.2 / 11.1, 16 x 300 x 28000 10.9 / 25.4, 1 x 8192 x 28672 38.5 / 34.3.  A
+// second launch costs the host some 5 us, more than that saves below kGemvPre
+// pieces of 128 weight rows x 256 channels unless the rows are long; so with more
+// than 16 rows always, with more than 4 from kGemvPre or kGemvLong on.
+constexpr int64_t kGemvPre = 1024, kGemvLong = 8192;
 
 template <int RT, int NT, bool PRE, bool F32>
 std::atomic<int> g_gemv_set[kMaxDevices];
@@ -2841,7 +2843,7 @@ int gemv_tiles(int64_t M) { return M <= 8 ? 1 : M <= 16 ? 2 : 4; }
 
 bool gemv_pre(int64_t M, int64_t N, int64_t K)
 {
-    return M > 8 || (M > 4 && (N + 127) / 128 * ((K + 255) / 256) >= kGemvPre);
+    return M > 16 || (M > 4 && (K >= kGemvLong || (N + 127) / 128 * ((K + 255) / 256) >= kGemvPre));
 }
 
 // Row tiles per CTA and ranks per cluster.  A CTA's x is 2 M / (17/32 x 16 RT)
@@ -2862,19 +2864,19 @@ int gemv_rows(const char *fn, const GemvArgs &a, int sms)
     int rt = 8;
     while (rt > kMinRT && int64_t(groups) * (gemv::kWarps / rt) * ranks(rt) < sms) rt /= 2;
     const int parts = groups * (gemv::kWarps / rt), S = ranks(rt);
-    if (NT > 1 || gemv_pre(a.M, a.N, a.K)) {
+    if (NT == 4 || gemv_pre(a.M, a.N, a.K)) {
         switch (rt) {
         case 8: return gemv_launch<8, NT, true, F32>(fn, a, parts, S);
         case 4: return gemv_launch<4, NT, true, F32>(fn, a, parts, S);
         case 2: if constexpr (kMinRT <= 2) return gemv_launch<2, NT, true, F32>(fn, a, parts, S); break;
         default: if constexpr (kMinRT <= 1) return gemv_launch<1, NT, true, F32>(fn, a, parts, S); break;
         }
-    } else if constexpr (NT == 1) {
+    } else if constexpr (NT < 4) {
         switch (rt) {
-        case 8: return gemv_launch<8, 1, false, F32>(fn, a, parts, S);
-        case 4: return gemv_launch<4, 1, false, F32>(fn, a, parts, S);
-        case 2: return gemv_launch<2, 1, false, F32>(fn, a, parts, S);
-        default: return gemv_launch<1, 1, false, F32>(fn, a, parts, S);
+        case 8: return gemv_launch<8, NT, false, F32>(fn, a, parts, S);
+        case 4: return gemv_launch<4, NT, false, F32>(fn, a, parts, S);
+        case 2: return gemv_launch<2, NT, false, F32>(fn, a, parts, S);
+        default: if constexpr (NT == 1) return gemv_launch<1, 1, false, F32>(fn, a, parts, S); break;
         }
     }
     return fail(KQ_ERR_VARIANT, "%s: no such row tile", fn);
