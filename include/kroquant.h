@@ -315,7 +315,7 @@ typedef struct {
  *               block_table[b][p / page_size].  An entry outside
  *               [0, num_pages) is no page.
  * The values are bounded on the device: a position before 0, behind the
- * table's row or on no page is skipped.  max_pages * page_size < 2^31. */
+ * table's row or on no page is skipped.  max_pages * page_size <= 2^31 - 2^20. */
 typedef struct {
     const int32_t *block_table;
     int64_t table_stride, max_pages;

@@ -630,3 +630,89 @@ def test_attention_items_of_one_and_two_tiles_in_turn(cuda_device, hkv, new):
     p = Plan([1500, 0, 130], [new, new, new // 2], hkv, 64, 16, seed=70)
     attend(p, normal(p.T, 4 * hkv, 64, key=70), max_new=new)
     assert kq.kq_wait_timeouts() == 0
+
+
+def test_a_pool_without_pages_holds_nothing(cuda_device):
+    """No pages at all: nothing is written, zeros are read and attended."""
+    kc, ks = torch.empty(0, 2, 16, 32, dtype=torch.uint8, device="cuda"), torch.empty(0, 2, 16, 2, dtype=torch.uint8, device="cuda")
+    table = torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+    for new in (1, 40):
+        cu, lens = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, new], [new]))
+        x = normal(new, 4, 64, key=new)
+        kq.mx_cache_write(x[:, :2], x[:, 2:], kc, ks, kc, ks, table, cu, lens)
+        assert (kq.mx_cache_read(kc, ks, kc, ks, table, cu, new)[1] == 0).all()
+        assert (kq.mx_paged_attention(x, kc, ks, kc, ks, table, cu, lens) == 0).all()
+
+
+def test_calls_side_by_side(cuda_device):
+    """Chunks, single tokens, products of both kinds on streams of their own at once, each with its own workspace."""
+    plans = [Plan([900, 30], [200, 90], 2, 128, 64, seed=80), Plan([2000] * 5, [1] * 5, 2, 128, 64, seed=81),
+             Plan([100], [300], 4, 64, 16, seed=82)]
+    qs = [normal(p.T, 4 * p.H, p.d, key=83) for p in plans]
+    w, wsf = kq.mx_quantize_f32(torch.randn(3000, 2048, device="cuda", generator=rng(84)), sf_layout=True)
+    xs = [normal(m, 2048, key=m) for m in (3, 12, 30)]
+    a, asc = kq.mx_quantize(normal(256, 2048, key=85))
+    a_sf = kq.mx_scales_to_sf(asc)
+    want = [kq.mx_paged_attention(q, *p.args, max_new=max(p.new)) for p, q in zip(plans, qs)] + [kq.mxf4_gemv(x, w, wsf) for x in xs]
+    want.append(kq.mxf4_gemm(a, a_sf, w, wsf))
+    torch.cuda.synchronize()
+    outs = [torch.zeros_like(t) for t in want]
+    streams = [torch.cuda.Stream() for _ in want]
+    work = [torch.empty(kq.mx_attention_workspace(p.T, 4 * p.H, p.H, p.d, max(p.new)), dtype=torch.uint8, device="cuda") for p in plans]
+    work += [torch.empty(kq.mxf4_gemv_workspace(x.shape[0], 3000, 2048), dtype=torch.uint8, device="cuda") for x in xs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            if i < 3:
+                kq.mx_paged_attention(qs[i], *plans[i].args, max_new=max(plans[i].new), out=outs[i], workspace=work[i], stream=s)
+            elif i < 6:
+                kq.mxf4_gemv(xs[i - 3], w, wsf, out=outs[i], workspace=work[i], stream=s)
+            else:
+                kq.mxf4_gemm(a, a_sf, w, wsf, out=outs[i], stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(outs, want)) and kq.kq_wait_timeouts() == 0
+
+
+def test_captured_chunks_and_converted_products(cuda_device):
+    """A chunk over a cache and a product that converts its rows beforehand, captured twice and replayed over new inputs."""
+    N, K, M = 700, 1024, 24
+    w, wsf = kq.mx_quantize_f32(torch.randn(N, K, device="cuda", generator=rng(90)), sf_layout=True)
+    steps = [(Plan([500 + i, 60], [70, 33], 2, 64, 16, seed=91 + i), normal(103, 8, 64, key=92 + i), normal(M, K, key=94 + i)) for i in range(2)]
+
+    def step(p, q, x):
+        return kq.mx_paged_attention(q, *p.args, max_new=70), kq.mxf4_gemv(x, w, wsf)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for s in steps:
+            step(*s)
+    torch.cuda.synchronize()
+    graphs = []
+    for s in steps:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = step(*s)
+        graphs.append((g, res))
+    for r in range(3):
+        for p, q, x in steps:
+            q.copy_(normal(*q.shape, key=200 + r))
+            x.copy_(normal(*x.shape, key=300 + r))
+        want = [[t.clone() for t in step(*s)] for s in steps]
+        for g, _ in graphs:
+            g.replay()
+        for (_, res), ww in zip(graphs, want):
+            assert all(torch.equal(a, b) for a, b in zip(res, ww))
+    assert kq.kq_wait_timeouts() == 0
+
+
+def test_attention_of_wide_value_ranges_among_ordinary_ones(cuda_device):
+    """Stages whose value scales lie further apart than fp16 takes beside stages that do not, zero blocks and the smallest scales among them."""
+    for spread in (6, 12, 13, 14, 40, 126):
+        p = Plan([1500], [2], 2, 128, 32, seed=spread)
+        pos = torch.arange(p.lens[0], device="cuda")
+        pg, at = p.table[0][pos // 32].long(), pos % 32
+        p.vs[pg, :, at] = 127
+        low = (pos // 64) % 3 == 1
+        p.vs[pg[low], :, at[low]] = 127 - spread
+        p.vs[pg[pos % 50 == 7], :, at[pos % 50 == 7], 1] = 0
+        attend(p, normal(p.T, 8, 128, key=spread), max_new=2)

@@ -56,7 +56,7 @@ def test_gemv_refusals(L):
 
 SHAPES = [dict(d=48), dict(d=160), dict(d=0), dict(heads=0), dict(heads=65536), dict(page=8), dict(page=24), dict(page=0),
           dict(page=1 << 21), dict(pages=-1), dict(pages=1 << 31)]
-BATCHES = [dict(B=-1), dict(pages=-1), dict(pages=4), dict(stride=1 << 32, pages=1 << 31), dict(stride=1 << 27, pages=1 << 27)]
+BATCHES = [dict(B=-1), dict(pages=-1), dict(pages=4), dict(stride=1 << 32, pages=1 << 31), dict(stride=1 << 27, pages=1 << 27), dict(stride=(1 << 27) - (1 << 16) + 1, pages=(1 << 27) - (1 << 16) + 1)]
 
 
 def write(L, c, b, k=16, v=16, st=128, sh=64, f32=0, T=4):
@@ -112,6 +112,7 @@ def test_attention_refusals(L):
     assert attend(L, cache(), batch(), hq=3) == -2 and "heads_q" in err(L)
     assert attend(L, cache(), batch(), hq=0) == -2 and attend(L, cache(), batch(), hq=-4) == -2
     assert attend(L, cache(), batch(), max_new=-1) == -2
+    assert attend(L, cache(), batch(), T=(1 << 31) - 1, hq=4) == -2 and attend(L, cache(), batch(), scale=3e38) == -2
     assert attend(L, cache(), batch(), scale=float("nan")) == -2 and attend(L, cache(), batch(), scale=float("inf")) == -2
     assert attend(L, cache(), batch(), q=None) == -1 and attend(L, cache(), batch(), o=None) == -1
     assert attend(L, cache(), batch(), q=8) == -3 and attend(L, cache(), batch(), o=8) == -3

@@ -2681,6 +2681,9 @@ int norm_launch(const char *fn, const void *h_bf16, const float *gamma, const fl
 // MXFP4 block) up to 128.
 bool head_dim_ok(int64_t D) { return D == 32 || D == 64 || D == 96 || D == 128; }
 
+// Positions of a sequence: a few stages past the last one still fit 32 bits.
+constexpr int64_t kMaxPositions = (int64_t(1) << 31) - (1 << 20);
+
 // Checks of a cache and a batch that need no pointer; fills `s`.
 int check_seqs(const char *fn, const mx_cache *c, const mx_batch *b, int64_t T, cache::Seqs *s)
 {
@@ -2696,8 +2699,8 @@ int check_seqs(const char *fn, const mx_cache *c, const mx_batch *b, int64_t T, 
         return fail(KQ_ERR_SHAPE, "%s: page_size must be a multiple of 16 up to 2^20 (got %lld)", fn,
                     (long long)c->page_size);
     if (c->num_pages < 0 || c->num_pages >= (int64_t(1) << 31) || b->max_pages < 0 ||
-        b->max_pages >= (int64_t(1) << 31) || b->max_pages * c->page_size >= (int64_t(1) << 31))
-        return fail(KQ_ERR_SHAPE, "%s: need 0 <= num_pages < 2^31 and 0 <= max_pages * page_size < 2^31 "
+        b->max_pages >= (int64_t(1) << 31) || b->max_pages * c->page_size > kMaxPositions)
+        return fail(KQ_ERR_SHAPE, "%s: need 0 <= num_pages < 2^31 and 0 <= max_pages * page_size <= 2^31 - 2^20 "
                     "(num_pages=%lld, max_pages=%lld)", fn, (long long)c->num_pages, (long long)b->max_pages);
     if (b->table_stride < b->max_pages || b->table_stride >= (int64_t(1) << 31))
         return fail(KQ_ERR_SHAPE, "%s: table_stride is below max_pages", fn);
@@ -2707,7 +2710,7 @@ int check_seqs(const char *fn, const mx_cache *c, const mx_batch *b, int64_t T, 
     s->len = b->seq_lens;
     s->B = int(b->batch);
     s->T = int(T);
-    s->max_pages = int(b->max_pages);
+    s->max_pages = c->num_pages > 0 ? int(b->max_pages) : 0;     // (a pool without pages holds no position)
     s->num_pages = int(c->num_pages);
     s->page = int(c->page_size);
     s->heads = int(c->heads);
@@ -3470,7 +3473,10 @@ int mx_paged_attention(const void *q_bf16, int64_t q_stride_t, int64_t q_stride_
         return fail(KQ_ERR_SHAPE, "%s: heads_q must be a positive multiple of the cache's heads (%lld, %lld)", fn,
                     (long long)heads_q, (long long)c->heads);
     if (max_new < 0) return fail(KQ_ERR_SHAPE, "%s: max_new must not be negative", fn);
-    if (!(std::isfinite(scale))) return fail(KQ_ERR_SHAPE, "%s: scale must be finite", fn);
+    if (T * (heads_q / c->heads) >= (int64_t(1) << 31))
+        return fail(KQ_ERR_SHAPE, "%s: T * heads_q / heads must be below 2^31 (T=%lld)", fn, (long long)T);
+    const float scale_log2 = scale * 1.44269504088896340736f;    // scores in units of log 2
+    if (!std::isfinite(scale_log2)) return fail(KQ_ERR_SHAPE, "%s: scale must be finite, also times log2(e)", fn);
     if (T == 0 || b->batch == 0) return ok();
     if ((rc = check_seq_pointers(fn, c, b, true)) != KQ_OK) return rc;
     if ((rc = check_strided(fn, "q", q_bf16, q_stride_t, q_stride_h, 2)) != KQ_OK) return rc;
@@ -3491,7 +3497,7 @@ int mx_paged_attention(const void *q_bf16, int64_t q_stride_t, int64_t q_stride_
     a.vc = c->v_codes;
     a.vs = c->v_scales;
     a.out = static_cast<__nv_bfloat16 *>(out_bf16);
-    a.scale_log2 = scale * 1.44269504088896340736f;
+    a.scale_log2 = scale_log2;
     a.causal = causal != 0;
     a.hq = int(heads_q);
     a.group = int(heads_q / c->heads);
