@@ -471,9 +471,12 @@ few_kernel(const Args a)
             uint32_t bits = 0;
             if (t0 < t_end) {
                 const uint32_t dst = ring_s + slot_i * C::kStage;
+                int64_t row = -1;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {                // strips of 16 positions, contiguous in the pool
-                    const int64_t row = t0 + 16 * s < t_end ? strip_row(a, table, p.h, t0 + 16 * s) : -1;
+                    // (pages of 32 positions and more: a stage is on one)
+                    if (s == 0 || a.page_shift < 5) row = t0 + 16 * s < t_end ? strip_row(a, table, p.h, t0 + 16 * s) : -1;
+                    else row = row >= 0 && t0 + 16 < t_end ? row + 16 : -1;
                     const uint32_t size = row >= 0 ? 16 : 0;
                     bits |= row >= 0 ? 1u << s : 0u;
                     const int64_t at = row >= 0 ? row : 0;
@@ -515,83 +518,103 @@ few_kernel(const Args a)
             // ---- scales of the stage: lane = position
             const bool valid = t0 + lane < t_end && ((pages >> (lane >> 4)) & 1);
             const uint32_t mask = __ballot_sync(0xffffffffu, valid);
-            int kb[NB], vb[NB], ktop = 0, vmax = 0, vmin = 255;
-            bool vnan = false;
+            // bytes 0, 2 and 1, 3 of the position's scales as 16-bit pairs (0 where it counts for nothing: its P is 0)
+            uint32_t k2[2], v2[2];
             {
                 const uint8_t *ks = st + 2 * C::kBytes + lane * NB;
+                uint32_t wk = 0, wv = 0;
                 if constexpr (NB == 4) {
-                    const uint32_t wk = *reinterpret_cast<const uint32_t *>(ks);
-                    const uint32_t wv = *reinterpret_cast<const uint32_t *>(ks + C::kScaleBytes);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        kb[b] = (wk >> (8 * b)) & 0xff;
-                        vb[b] = (wv >> (8 * b)) & 0xff;
-                    }
+                    wk = *reinterpret_cast<const uint32_t *>(ks);
+                    wv = *reinterpret_cast<const uint32_t *>(ks + C::kScaleBytes);
                 } else {
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
-                        kb[b] = ks[b];
-                        vb[b] = ks[C::kScaleBytes + b];
+                        wk |= uint32_t(ks[b]) << (8 * b);
+                        wv |= uint32_t(ks[C::kScaleBytes + b]) << (8 * b);
                     }
                 }
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    if (kb[b] < int(kNanByte)) ktop = max(ktop, kb[b]);
-                    if (vb[b] >= int(kNanByte)) vnan = true;
-                    else if (vb[b] > 0) {
-                        vmax = max(vmax, vb[b]);
-                        vmin = min(vmin, vb[b]);
-                    }
-                }
-                if (!valid) {
-                    ktop = vmax = 0;
-                    vmin = 255;
-                    vnan = false;
-                }
+                wk = valid ? wk : 0u;
+                wv = valid ? wv : 0u;
+                k2[0] = wk & 0x00ff00ffu, k2[1] = (wk >> 8) & 0x00ff00ffu;
+                v2[0] = wv & 0x00ff00ffu, v2[1] = (wv >> 8) & 0x00ff00ffu;
             }
-            if (__any_sync(0xffffffffu, vnan || vmax > vtop || ktop > kref)) {
-                // rare but for the first stages: values that are NaN, which count as zero here, and larger scales
-                if (vnan) {
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        if (vb[b] >= int(kNanByte)) {
-                            atomicMin(&nan_first[b], t0 + lane);
-                            vb[b] = -512;
-                        }
-                }
-                ktop = __reduce_max_sync(0xffffffffu, ktop);
-                if (ktop > kref) {
-                    kref = ktop;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) cs[t][i] = a.scale_log2 * pow2(max(min(qe[t][i] + kref - 127, 127), -126));
-                }
-                vmax = __reduce_max_sync(0xffffffffu, vmax);
-                if (vmax > vtop) {
-                    const float f = pow2(vtop - vmax);
-                    vtop = vmax;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[t][i][e] *= f;
-                }
-            }
-            const bool wide = __any_sync(0xffffffffu, vmin < vtop - kWindow);
+            uint32_t knan = 0;                               // blocks of the position that are NaN
             {
-                float kv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const uint32_t km = __vmaxu2(k2[0], k2[1]), vm = __vmaxu2(v2[0], v2[1]);
+                if (__any_sync(0xffffffffu, max(km >> 16, km & 0xffffu) > uint32_t(kref) || max(vm >> 16, vm & 0xffffu) > uint32_t(vtop))) {
+                    // rare but for the first stages: larger scales, and NaN (253 and more; such values count as zero here)
+                    int ktop = 0, vmax = 0;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const int ke = max(kb[b] - kref + 127, 0);
-                    kv[b] = __uint_as_float(kb[b] >= int(kNanByte) ? 0x7fc00000u : uint32_t(ke) << 23);
-                    // fp16 2^(byte - vtop) or bf16 2^(126 + byte - vtop), zero for a position that counts for nothing
-                    const int e = valid ? vb[b] - vtop : -512;
-                    const uint32_t f = wide ? uint32_t(max(e + 253, 0)) << 7 : uint32_t(max(e + 15, 0)) << 10;
-                    reinterpret_cast<uint16_t *>(vtab)[((lane >> 1) * 4 + b) * 2 + (lane & 1)] = uint16_t(f);
+                    for (int b = 0; b < NB; ++b) {
+                        const int sh = 16 * (b >> 1), kb = (k2[b & 1] >> sh) & 0xff, vb = (v2[b & 1] >> sh) & 0xff;
+                        if (kb >= int(kNanByte)) {
+                            knan |= 1u << b;
+                            k2[b & 1] &= ~(0xffu << sh);
+                        } else {
+                            ktop = max(ktop, kb);
+                        }
+                        if (vb >= int(kNanByte)) {
+                            atomicMin(&nan_first[b], t0 + lane);
+                            v2[b & 1] &= ~(0xffu << sh);
+                        } else {
+                            vmax = max(vmax, vb);
+                        }
+                    }
+                    ktop = __reduce_max_sync(0xffffffffu, ktop);
+                    if (ktop > kref) {
+                        kref = ktop;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) cs[t][i] = a.scale_log2 * pow2(max(min(qe[t][i] + kref - 127, 127), -126));
+                    }
+                    vmax = __reduce_max_sync(0xffffffffu, vmax);
+                    if (vmax > vtop) {
+                        const float f = pow2(vtop - vmax);
+                        vtop = vmax;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[t][i][e] *= f;
+                    }
                 }
+            }
+            // a block with 0 < scale < vtop - kWindow: bit 8 of (scale + 255), and not of scale + 256 - the limit
+            bool wide;
+            {
+                const uint32_t limit = uint32_t(256 - max(vtop - kWindow, 0)) * 0x00010001u;
+                const uint32_t low = ((v2[0] + 0x00ff00ffu) & ~(v2[0] + limit)) | ((v2[1] + 0x00ff00ffu) & ~(v2[1] + limit));
+                wide = __any_sync(0xffffffffu, (low & 0x01000100u) != 0);
+            }
+            {
+                // exponents relative to the largest, by pairs: max(scale, ref - e0) - (ref - e0) is the field of 2^(scale - ref)
+                // where e0 is that of 1, and 0 below
+                auto fields = [](uint32_t x, int ref, int e0) {
+                    return __vmaxu2(x, uint32_t(max(ref - e0, 0)) * 0x00010001u) + uint32_t(e0 - ref) * 0x00010001u;
+                };
+                const uint32_t k02 = fields(k2[0], kref, 127), k13 = fields(k2[1], kref, 127);
+                float kv[4] = {__uint_as_float(k02 << 23), __uint_as_float(k13 << 23), __uint_as_float((k02 << 7) & 0x7f800000u),
+                               __uint_as_float((k13 << 7) & 0x7f800000u)};
+                if (knan)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        if ((knan >> b) & 1) kv[b] = __uint_as_float(0x7fc00000u);
                 *reinterpret_cast<float4 *>(ktab + 4 * lane) = make_float4(kv[0], kv[1], kv[2], kv[3]);
+                // fp16 2^(scale - vtop) or bf16 2^(126 + scale - vtop); two positions to a word
+                uint32_t f02, f13;
+                if (!wide) {
+                    f02 = fields(v2[0], vtop, 15) << 10;
+                    f13 = fields(v2[1], vtop, 15) << 10;
+                } else {
+                    f02 = (v2[0] + uint32_t(253 - vtop) * 0x00010001u) << 7;
+                    f13 = (v2[1] + uint32_t(253 - vtop) * 0x00010001u) << 7;
+                }
+                const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
+                const uint32_t w0 = __byte_perm(f02, __shfl_xor_sync(0xffffffffu, f02, 1), sel);
+                const uint32_t w1 = __byte_perm(f13, __shfl_xor_sync(0xffffffffu, f13, 1), sel);
+                *reinterpret_cast<uint2 *>(vtab + (lane >> 1) * 4 + (lane & 1) * 2) = make_uint2(w0, w1);
             }
             __syncwarp();
 
