@@ -83,6 +83,43 @@ __device__ __forceinline__ bool row_place(const Seqs &s, int t, const int32_t *s
     return true;
 }
 
+// A lane's pieces p0, p0 + 32, ...: 32 pieces are whole heads (but for three
+// blocks to a head), so that a place is the first one's and a multiple of a
+// stride: what finds it was most of the instructions otherwise.
+template <int NB>
+struct Lane {
+    static constexpr int PH = 4 * NB;        // pieces of a head
+    int h, c;                                // head and place in it of piece p0
+
+    __device__ __forceinline__ Lane(int p0) : h(p0 / PH), c(p0 % PH) {}
+    // for piece p0 + 32 i: the number of heads further, and the place
+    __device__ __forceinline__ int heads(int i) const { return 32 % PH == 0 ? i * (32 / PH) : (c + 32 * i) / PH; }
+    __device__ __forceinline__ int place(int i) const { return 32 % PH == 0 ? c : (c + 32 * i) % PH; }
+};
+
+// Eight codes as bf16 pairs in order, times 2^(sb - 127); NaN for 255.  (Exact; as
+// two factors, for bf16 takes code * 2^-126 to at most code * 2 in one.)
+__device__ __forceinline__ uint4 decode_bf16(uint32_t w, uint32_t sb)
+{
+    auto mul = [](uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    };
+    // one AND, one multiply and one AND put codes n and n + 4 side by side as bf16 numbers code * 2^-126
+    constexpr uint32_t kA = (1u << 12) + (1u << 6), kB = (1u << 8) + (1u << 2), kM = 0x81C081C0u;
+    const uint32_t f = (min(sb, 128u) + 126u) * 0x00800080u, v = w >> 8;
+    uint32_t x[4] = {mul(((w & 0x000F000Fu) * kA) & kM, f), mul(((w & 0x00F000F0u) * kB) & kM, f),
+                     mul(((v & 0x000F000Fu) * kA) & kM, f), mul(((v & 0x00F000F0u) * kB) & kM, f)};
+    if (sb > 128u) {
+        const uint32_t f2 = sb == 255u ? 0x7fc07fc0u : (sb - 1u) * 0x00800080u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = mul(x[i], f2);
+    }
+    return make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[0], x[1], 0x7632),
+                      __byte_perm(x[2], x[3], 0x7632));
+}
+
 // Quantize the keys and values of new tokens into the cache, as the other MXFP4
 // kernels do: the four lanes of a block share its largest magnitude (bits order
 // like magnitudes, and what is not finite is above all that is).
@@ -106,12 +143,13 @@ write_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t kst
         uint32_t *codes = is_v ? vc : kc;
         uint8_t *scales = is_v ? vs : ks;
         for (int p0 = lane; p0 - lane < pieces; p0 += 32 * kPieces) {
+            const Lane<NB> of(p0);
+            const int64_t src0 = src + of.h * sh, row0 = row + int64_t(of.h) * s.page;
             float x[kPieces][8];
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-                const int p = p0 + 32 * i, h = p / PH, c = p % PH;
-                const int64_t at = src + int64_t(h) * sh + 8 * c;
-                if (p < pieces) {
+                const int64_t at = src0 + of.heads(i) * sh + 8 * of.place(i);
+                if (p0 + 32 * i < pieces) {
                     if constexpr (F32) {
                         const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(in) + at);
                         const float4 u = __ldg(q), w = __ldg(q + 1);
@@ -130,13 +168,13 @@ write_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t kst
             }
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-                const int p = p0 + 32 * i, h = p / PH, c = p % PH;
+                const int c = of.place(i);
                 uint32_t top = 0;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7fffffffu);
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                if (p >= pieces) continue;
+                if (p0 + 32 * i >= pieces) continue;
                 uint32_t sb = 0xFFu, w = 0;
                 if (top < 0x7f800000u) {
                     sb = e8m0_byte(__uint_as_float(top));
@@ -144,7 +182,7 @@ write_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t kst
                     w = cvt_e2m1x8(x[i][0] * f, x[i][1] * f, x[i][2] * f, x[i][3] * f, x[i][4] * f, x[i][5] * f, x[i][6] * f,
                                    x[i][7] * f);
                 }
-                const int64_t to = row + int64_t(h) * s.page;
+                const int64_t to = row0 + of.heads(i) * int64_t(s.page);
                 codes[to * PH + c] = w;
                 if (c % 4 == 0) scales[to * NB + c / 4] = uint8_t(sb);
             }
@@ -174,38 +212,37 @@ read_kernel(const uint32_t *__restrict__ kc, const uint8_t *__restrict__ ks, con
         const uint8_t *scales = is_v ? vs : ks;
         void *out = is_v ? out_v : out_k;
         for (int p0 = lane; p0 < pieces; p0 += 32 * kPieces) {
+            const Lane<NB> of(p0);
+            const int64_t row0 = row + int64_t(of.h) * s.page;
             uint32_t w[kPieces], sb[kPieces];
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-                const int p = p0 + 32 * i, h = p / PH, c = p % PH;
                 w[i] = sb[i] = 0;
-                if (p < pieces && row >= 0) {
-                    const int64_t at = row + int64_t(h) * s.page;
-                    w[i] = __ldg(codes + at * PH + c);
-                    sb[i] = __ldg(scales + at * NB + c / 4);
+                if (p0 + 32 * i < pieces && row >= 0) {
+                    const int64_t at = row0 + of.heads(i) * int64_t(s.page);
+                    w[i] = __ldg(codes + at * PH + of.place(i));
+                    sb[i] = __ldg(scales + at * NB + of.place(i) / 4);
                 }
             }
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int p = p0 + 32 * i;
                 if (p >= pieces) break;
-                const float f = e8m0_value(sb[i]);
-                float2 e[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    e[j] = e2m1x2_to_f32x2((w[i] >> (8 * j)) & 0xFFu);
-                    e[j].x *= f;
-                    e[j].y *= f;
-                }
                 const int64_t to = int64_t(t) * pieces + p;
                 if constexpr (F32) {
+                    const float f = e8m0_value(sb[i]);
+                    float2 e[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        e[j] = e2m1x2_to_f32x2((w[i] >> (8 * j)) & 0xFFu);
+                        e[j].x *= f;
+                        e[j].y *= f;
+                    }
                     float4 *o = static_cast<float4 *>(out) + to * 2;
                     o[0] = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
                     o[1] = make_float4(e[2].x, e[2].y, e[3].x, e[3].y);
                 } else {
-                    static_cast<uint4 *>(out)[to] =
-                        make_uint4(mma::pack_bf16x2(e[0].x, e[0].y), mma::pack_bf16x2(e[1].x, e[1].y),
-                                   mma::pack_bf16x2(e[2].x, e[2].y), mma::pack_bf16x2(e[3].x, e[3].y));
+                    static_cast<uint4 *>(out)[to] = decode_bf16(w[i], sb[i]);
                 }
             }
         }

@@ -246,7 +246,7 @@ chunk_kernel(const Args a, long long budget)
     extern __shared__ __align__(16) uint8_t smem_dyn[];
     __shared__ int64_t sh[kThreads + 34];
     __shared__ uint32_t tmem_slot;
-    __shared__ uint32_t visible[4][4];       // of step s % 4: the positions that are on a page, 32 to a word
+    __shared__ __align__(16) uint32_t visible[4][4];         // of step s % 4: the positions that are on a page, 32 to a word
     __shared__ int nan_first[kSegs][4];      // of segment i % kSegs, per 32 channels: the first position whose value is NaN
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = base, *sK = base + 2 * C::kQBytes, *sV = sK + kRing * C::kStepBytes;
@@ -538,7 +538,8 @@ chunk_kernel(const Args a, long long budget)
                     mma::tc_fence_after();
                     const uint32_t *on = visible[(k + u) & 3];
                     float x[32], y[32];
-                    if (lim_min < kStep || (on[0] & on[1] & on[2] & on[3]) != 0xffffffffu) {
+                    const uint4 all = *reinterpret_cast<const uint4 *>(on);
+                    if (lim_min < kStep || (all.x & all.y & all.z & all.w) != 0xffffffffu) {
                         // rare: what the rows do not see becomes -infinity in tensor memory
 #pragma unroll 1
                         for (int j = 0; j < 4; ++j) {
