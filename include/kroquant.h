@@ -353,8 +353,9 @@ int mx_cache_read(const mx_cache *cache, const mx_batch *seqs, const int32_t *st
  * token t's own (causal != 0) or over all of the sequence's seq_lens[b].
  * q bf16 [T][heads_q][head_dim] with token and head strides (as for
  * mx_cache_write); out bf16 [T][heads_q][head_dim], contiguous.  Scores,
- * maxima and sums in fp32, the probabilities rounded to bf16 for the second
- * product.  A position on no page is not seen; a row that sees nothing is
+ * maxima and sums in fp32; for the second product the probabilities are
+ * rounded to bf16, or (few rows) multiplied by their values' scale and rounded
+ * to fp16: half a step of it, or 2^-40 of the largest value scale times 6.  A position on no page is not seen; a row that sees nothing is
  * zero; what a row does not see does not reach it, NaN or not.  K and V scale
  * bytes 253 to 255 (mx_cache_write writes none of the first two) read as NaN.
  * max_new: a bound on the new tokens of any one sequence (T does); it selects

@@ -2981,6 +2981,9 @@ int attn_launch(const char *fn, attn::Args a, int64_t max_new, cudaStream_t stre
 
 }  // namespace
 
+// ---------------------------------------------------------------------------
+// C ABI
+// ---------------------------------------------------------------------------
 extern "C" {
 
 int kq_abi_version(void) { return 1; }

@@ -39,6 +39,15 @@
 // Q, K and V lie in the 128-byte swizzle, 64 channels to a row of 128 bytes; K
 // and Q are read K-major, V with its channels as the major dimension.
 // Every wait is bounded (g_wait_timeouts).
+//
+// Measured, 32 query heads over 8 of 128 channels: 2048 tokens over 32,048
+// positions 0.88 ms, 1.18 PFLOP/s (0.72 of a cuBLAS bf16 product's burst rate,
+// 0.85 of its sustained one); 1024 over 31,000 0.45 ms; a causal prompt of 4096
+// 227 us.  A step of both tiles takes 4050 clocks: tensor pipe and exponential
+// unit 47 % busy, issue slots 49 %.  A tile's turn is Q K' (some 700 clocks with
+// P V before it), the softmax (3000, of which 2000 while the other tile's
+// exponentials compete), then P V.  An item costs some 16,000 clocks beside
+// its steps: queries, the first S, results.
 
 namespace attn {
 namespace chunk {
