@@ -14,6 +14,15 @@ from w4a4_mxfp4_post_b200 import synth
 
 pytestmark = pytest.mark.gpu
 
+
+@pytest.fixture(autouse=True, params=["native", "python"])
+def binding(request, monkeypatch):
+    """Every test through both ways of the binding: its native part, and the Python calls."""
+    if request.param == "python":
+        monkeypatch.setattr(kq, "_native", lambda: False)
+    else:
+        assert kq._native(), "the binding's native part is not built"
+
 NAN = float("nan")
 
 
@@ -716,3 +725,45 @@ def test_attention_of_wide_value_ranges_among_ordinary_ones(cuda_device):
         p.vs[pg[low], :, at[low]] = 127 - spread
         p.vs[pg[pos % 50 == 7], :, at[pos % 50 == 7], 1] = 0
         attend(p, normal(p.T, 8, 128, key=spread), max_new=2)
+
+
+def test_native_binding_leaves_the_unusual_to_python(cuda_device):
+    """Wrong types and shapes are refused with the same errors either way; subclasses and strided tables work."""
+    p = Plan([40], [3], 2, 64, 16, seed=95, table_pad=4)
+    q = normal(3, 8, 64, key=95)
+    want = kq.mx_paged_attention(q, *p.args, max_new=3)
+    assert torch.equal(kq.mx_paged_attention(torch.nn.Parameter(q, requires_grad=False), *p.args), want)
+
+    class Sub(torch.Tensor):
+        pass
+
+    assert torch.equal(kq.mx_paged_attention(q.as_subclass(Sub), *p.args).as_subclass(torch.Tensor), want)
+    with pytest.raises(TypeError):
+        kq.mx_paged_attention(q.float(), *p.args)
+    with pytest.raises(TypeError):
+        kq.mx_paged_attention(q, *p.cache, p.table.long(), p.cud, p.lensd)
+    with pytest.raises(ValueError):
+        kq.mx_paged_attention(q, *p.cache, p.table, p.cud[:1], p.lensd)
+    with pytest.raises(ValueError):
+        kq.mx_paged_attention(q[:, :3], *p.args)
+    with pytest.raises(ValueError):
+        kq.mx_paged_attention(q, *p.args, max_new=-1)
+    with pytest.raises(kq.KroQuantError):
+        kq.mx_paged_attention(q, *p.args, scale=float("inf"))
+    with pytest.raises(TypeError):
+        kq.mx_paged_attention(q, *p.cache, p.table, p.cud, None)
+    with pytest.raises(ValueError):
+        kq.mx_cache_write(q, q, *p.args)
+    with pytest.raises(TypeError):
+        kq.mx_cache_write(q[:, :2], q[:, 2:4].float(), *p.args)
+    with pytest.raises((ValueError, RuntimeError)):
+        kq.mx_cache_read(*p.cache, p.table, p.cud, -1)
+    w, wsf = kq.mx_quantize_f32(torch.randn(64, 512, device="cuda"), sf_layout=True)
+    x = normal(5, 512, key=96)
+    assert torch.equal(kq.mxf4_gemv(x, w, wsf, out_dtype=torch.float32).bfloat16(), kq.mxf4_gemv(x, w, wsf))
+    with pytest.raises(ValueError):
+        kq.mxf4_gemv(x[:, :256], w, wsf)
+    with pytest.raises(ValueError):
+        kq.mxf4_gemv(x, w, wsf[:-1])
+    with pytest.raises(kq.KroQuantError):
+        kq.mxf4_gemv(normal(33, 512, key=97), w, wsf)

@@ -575,6 +575,11 @@ def mxf4_gemv(x, b_codes, b_sf, out=None, out_dtype=None, workspace=None, stream
     tensor of mxf4_gemv_workspace(M, N, K) bytes for this call alone; allocated if None.
     """
     torch = _torch()
+    if out is None and workspace is None and stream is None and (out_dtype is None or out_dtype in (torch.bfloat16, torch.float32)):
+        native = _native()
+        done = native.gemv(x, b_codes, b_sf, out_dtype is torch.float32) if native else None
+        if done is not None:
+            return _done("mxf4_gemv", done)
     u8 = torch.uint8
     M, N = _gemv_sizes(x, b_codes, b_sf)
     K = x.shape[1]
@@ -595,6 +600,41 @@ def mxf4_gemv(x, b_codes, b_sf, out=None, out_dtype=None, workspace=None, stream
           f32, M, N, K,
           _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, dev))
     return out
+
+
+_native_module = None
+
+
+def _native():
+    """The binding's native part (csrc/binding.cpp), which does ordinary calls of the few-token
+    operators in one step and answers None to the others; False where it was not built."""
+    global _native_module
+    if _native_module is None:
+        import importlib.machinery
+        import importlib.util
+
+        from .build import binding_path
+
+        path = binding_path()
+        if not os.path.exists(path):
+            _native_module = False
+            return False
+        L = lib()
+        loader = importlib.machinery.ExtensionFileLoader("kq_binding", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("kq_binding", path, loader=loader))
+        loader.exec_module(module)
+        module.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "mxf4_gemv", "mxf4_gemv_workspace", "kq_sf_bytes", "mx_cache_write", "mx_cache_read", "mx_paged_attention",
+            "mx_attention_workspace")))
+        _native_module = module
+    return _native_module
+
+
+def _done(name, result):
+    """What a native call returned, or its error."""
+    if type(result) is int:
+        raise KroQuantError(name, result, kq_last_error())
+    return result
 
 
 def _gemv_sizes(x, b_codes, b_sf):
@@ -707,6 +747,12 @@ def mx_cache_write(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_s
     seq_lens int32 [B] (lengths with the new tokens, which are the last ones).
     """
     torch = _torch()
+    if stream is None:
+        native = _native()
+        done = native.write(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, seq_lens) if native else None
+        if done is not None:
+            _done("mx_cache_write", None if done is True else done)
+            return
     c, dev, H, D = _cache(k_codes, k_scales, v_codes, v_scales)
     if seq_lens is None:
         raise TypeError("seq_lens must be a torch.Tensor")
@@ -730,6 +776,12 @@ def mx_cache_read(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens,
     (starts int32 [B], default zeros) of sequence b.
     """
     torch = _torch()
+    if out_k is None and out_v is None and stream is None and (out_dtype is None or out_dtype in (torch.bfloat16, torch.float32)):
+        native = _native()
+        done = native.read(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, rows, starts,
+                           out_dtype is torch.float32) if native else None
+        if done is not None:
+            return _done("mx_cache_read", done)
     c, dev, H, D = _cache(k_codes, k_scales, v_codes, v_scales)
     b, B = _batch(block_table, cu_seqlens, None, dev)
     if starts is not None:
@@ -771,6 +823,12 @@ def mx_paged_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_
     tensor of mx_attention_workspace(...) bytes for this call alone; allocated if None.
     """
     torch = _torch()
+    if out is None and workspace is None and stream is None:
+        native = _native()
+        done = native.attention(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, seq_lens, max_new, scale,
+                                bool(causal)) if native else None
+        if done is not None:
+            return _done("mx_paged_attention", done)
     c, dev, H, D = _cache(k_codes, k_scales, v_codes, v_scales)
     if seq_lens is None:
         raise TypeError("seq_lens must be a torch.Tensor")

@@ -1,11 +1,16 @@
-"""Build the sm_100a CUDA library ``libkroquant.so`` in-tree (beside this file).
+"""Build the sm_100a CUDA library ``libkroquant.so`` in-tree (beside this file), and the
+binding's native part ``kq_binding.<torch version>.so``.
 
     python -m w4a4_mxfp4_post_b200.build [--force]
 
 The library is a plain shared object with the C ABI of ``include/kroquant.h``;
 it is compiled with nvcc for sm_100a only and links the CUDA runtime
-statically, so loading it needs no torch and no GPU.
+statically, so loading it needs no torch and no GPU.  The native part of the
+binding is host code against torch's headers; where torch is not installed it
+is left out, and the Python binding does its calls.
 """
+from __future__ import annotations
+
 import os
 import subprocess
 import sys
@@ -39,7 +44,39 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in SOURCES + HEADERS + [os.path.abspath(__file__)])
 
 
+def binding_path() -> str:
+    """The binding's native part: torch's ABI is in the name, for a file built against another must not load."""
+    from importlib.metadata import version
+
+    return os.path.join(HERE, f"kq_binding.{version('torch')}.so")
+
+
+def build_binding(force: bool = False) -> str | None:
+    """Compile csrc/binding.cpp; None without torch."""
+    import importlib.util
+    import sysconfig
+
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    out, src = binding_path(), os.path.join(HERE, "csrc", "binding.cpp")
+    deps = [src, os.path.join(INCLUDE, "kroquant.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps):
+        return out
+    torch_dir = os.path.dirname(spec.origin)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = out + ".tmp%d" % os.getpid()
+    subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", os.path.join(torch_dir, "include"),
+                    "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+                    "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), src,
+                    "-L", os.path.join(torch_dir, "lib"), "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda",
+                    "-o", tmp], check=True)
+    os.replace(tmp, out)
+    return out
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force)
     if not force and not _stale():
         return LIB
     tmp = LIB + ".tmp%d" % os.getpid()

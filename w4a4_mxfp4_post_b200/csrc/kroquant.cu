@@ -2796,7 +2796,7 @@ struct GemvArgs {
 // (GPU time): 32 x 1152 x 1152 8.2 / 10.9, 32 x 4096 x 4096 13.4 / 30, 16 x 8192 x
 // 28672 51 / 63, 16 x 4096 x 4096 10.4 / 12.0, 8 x 8192 x 28672 37 / 43, 8 x 4096 x
 // 4096 9.2 / 11.1, 16 x 300 x 28000 10.9 / 25.4, 1 x 8192 x 28672 38.5 / 34.3.  A
-// second launch costs the host some 5 us, more than that saves below kGemvPre
+// second launch costs the host 3 to 5 us, more than that saves below kGemvPre
 // pieces of 128 weight rows x 256 channels unless the rows are long; so with more
 // than 16 rows always, with more than 4 from kGemvPre or kGemvLong on.
 constexpr int64_t kGemvPre = 1024, kGemvLong = 8192;
