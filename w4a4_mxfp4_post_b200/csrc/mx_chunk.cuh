@@ -511,27 +511,30 @@ chunk_kernel(const Args a, long long budget)
                 // goes into it
                 {
                     const Seq q = walk.q;
-                    const int r = r0 + row, token = r / a.group, head = walk.p.h * a.group + r - token * a.group;
+                    const int r = r0 + row, rc = min(r, q.rows - 1), token = rc / a.group;
                     lim = r < q.rows ? row_end(a, q, r) - walk.t_first : 0x7fffffff;
-                    const int64_t from = int64_t(q.lo + token) * a.q_st + int64_t(head) * a.q_sh;
+                    const int64_t from = int64_t(q.lo + token) * a.q_st +
+                                         int64_t(walk.p.h * a.group + rc - token * a.group) * a.q_sh;
                     const uint32_t sgn = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-                    // lanes over the chunks of the warp's rows, so that every load is contiguous
-#pragma unroll 8
+                    const bool zero = a.scale_log2 == 0.0f;
+                    // lanes over the chunks of the warp's rows, so that every load is contiguous, and all loads
+                    // before the first use: one after the other they took 13k cycles an item, together 3.5k.  A row
+                    // that is not there reads the last one's, for nothing.
+                    uint4 w[D / 8];
+#pragma unroll
                     for (int e = 0; e < D / 8; ++e) {
                         const int pc = lane + 32 * e, rr = pc / (D / 8), ch = pc % (D / 8);
-                        const int64_t at = __shfl_sync(0xffffffffu, from, rr);
-                        const int rw = row - lane + rr;
-                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                        if (r0 + rw < q.rows) w = __ldg(reinterpret_cast<const uint4 *>(a.q + at) + ch);
-                        if (a.scale_log2 == 0.0f) {
-                            w.x = hmul2_bf16(w.x, 0u);
-                            w.y = hmul2_bf16(w.y, 0u);
-                            w.z = hmul2_bf16(w.z, 0u);
-                            w.w = hmul2_bf16(w.w, 0u);
-                        }
+                        w[e] = __ldg(reinterpret_cast<const uint4 *>(a.q + __shfl_sync(0xffffffffu, from, rr)) + ch);
+                    }
+#pragma unroll
+                    for (int e = 0; e < D / 8; ++e) {
+                        const int pc = lane + 32 * e, rr = pc / (D / 8), ch = pc % (D / 8), rw = row - lane + rr;
+                        if (zero)
+                            w[e] = make_uint4(hmul2_bf16(w[e].x, 0u), hmul2_bf16(w[e].y, 0u), hmul2_bf16(w[e].z, 0u),
+                                              hmul2_bf16(w[e].w, 0u));
                         *reinterpret_cast<uint4 *>(tile_q + rw * 128 + (ch / 8) * (kTile * 128) + (((ch % 8) ^ (rw & 7)) << 4)) =
-                            make_uint4(__byte_perm(w.x, w.z, 0x5410) ^ sgn, __byte_perm(w.x, w.z, 0x7632) ^ sgn,
-                                       __byte_perm(w.y, w.w, 0x5410) ^ sgn, __byte_perm(w.y, w.w, 0x7632) ^ sgn);
+                            make_uint4(__byte_perm(w[e].x, w[e].z, 0x5410) ^ sgn, __byte_perm(w[e].x, w[e].z, 0x7632) ^ sgn,
+                                       __byte_perm(w[e].y, w[e].w, 0x5410) ^ sgn, __byte_perm(w[e].y, w[e].w, 0x7632) ^ sgn);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
@@ -647,28 +650,25 @@ chunk_kernel(const Args a, long long budget)
                 const bool whole = walk.count == units;
                 float *sl = slot<R, D>(a, 2 * int(blockIdx.x) + (p.unit == 0 ? 1 : 0));
                 const int ir = i * kTile + row;                              // row of the item
-                const float inv = 1.0f / l;
+                // a row that has seen nothing has zeros (or NaN) in O: they stay
+                const float scale = !whole || l == 0.0f ? 1.0f : 1.0f / l;
                 if (!whole && mine) {
                     sl[R * D + ir] = m == -INFINITY ? m : m * c;
                     sl[R * D + R + ir] = l;
                 }
 #pragma unroll 1
-                for (int j = 0; j < 2 * NB; ++j) {
-                    float o[16];
-                    tmem_ld16(tO + 16 * j, o);
+                for (int j = 0; j < NB; ++j) {
+                    float o[32];
+                    mma::tmem_ld32_nowait(tO + 32 * j, o);
+                    const float f = nan_first[seg % kSegs][j] < sees ? __uint_as_float(0x7fc00000u) : scale;
                     tmem_wait_ld();
-                    const bool nan = nan_first[seg % kSegs][j / 2] < sees;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        // columns hold channels 0 4 1 5 2 6 3 7
-                        float v[8] = {o[8 * h], o[8 * h + 2], o[8 * h + 4], o[8 * h + 6],
-                                      o[8 * h + 1], o[8 * h + 3], o[8 * h + 5], o[8 * h + 7]};
+                    for (int h = 0; h < 4; ++h) {
+                        // columns hold channels 0 4 1 5 2 6 3 7; the sum makes a negative zero positive
+                        float v[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            if (nan) v[e] = __uint_as_float(0x7fc00000u);
-                            if (whole) v[e] = l == 0.0f && v[e] == 0.0f ? 0.0f : v[e] * inv;
-                        }
-                        const int ch = 2 * j + h;                            // of 8 channels
+                        for (int e = 0; e < 8; ++e) v[e] = fmaf(o[8 * h + 2 * (e % 4) + e / 4], f, 0.0f);
+                        const int ch = 4 * j + h;                            // of 8 channels
                         if (whole) {
                             // by way of Q's place, which the segment has done with, so that rows are written whole
                             *reinterpret_cast<uint4 *>(tile_q + row * 128 + (ch / 8) * (kTile * 128) + (((ch % 8) ^ (row & 7)) << 4)) =
@@ -684,12 +684,21 @@ chunk_kernel(const Args a, long long budget)
                 if (whole) {
                     const int token = r / a.group;
                     const int64_t to = (int64_t(q.lo + token) * a.hq + p.h * a.group + r - token * a.group) * D;
-#pragma unroll 4
-                    for (int e = 0; e < D / 8; ++e) {
-                        const int pc = lane + 32 * e, rr = pc / (D / 8), ch = pc % (D / 8), rw = row - lane + rr;
-                        const int64_t at = __shfl_sync(0xffffffffu, to, rr);
-                        const uint4 w = *reinterpret_cast<const uint4 *>(tile_q + rw * 128 + (ch / 8) * (kTile * 128) + (((ch % 8) ^ (rw & 7)) << 4));
-                        if (r0 + rw < q.rows) *reinterpret_cast<uint4 *>(a.out + at + 8 * ch) = w;
+#pragma unroll 1
+                    for (int e0 = 0; e0 < D / 8; e0 += 4) {
+                        uint4 w[4];
+                        int64_t at[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int pc = lane + 32 * (e0 + e), rr = pc / (D / 8), ch = pc % (D / 8), rw = row - lane + rr;
+                            w[e] = *reinterpret_cast<const uint4 *>(tile_q + rw * 128 + (ch / 8) * (kTile * 128) + (((ch % 8) ^ (rw & 7)) << 4));
+                            at[e] = __shfl_sync(0xffffffffu, to, rr) + 8 * ch;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int rr = (lane + 32 * (e0 + e)) / (D / 8);
+                            if (r0 + row - lane + rr < q.rows) *reinterpret_cast<uint4 *>(a.out + at[e]) = w[e];
+                        }
                     }
                     __syncwarp();
                 }
