@@ -18,7 +18,7 @@
 // the lengths on the device: no plan on the host, ragged batches balance, and
 // long sequences split over as many CTAs as they need.  (What an item costs beside
 // its units counts as units, too: a causal prompt of 4096, whose first items are
-// one unit long, took 368 us without, 227 with.)  A CTA whose share ends inside
+// one unit long, took 253 us without, 165 with.)  A CTA whose share ends inside
 // an item leaves a partial result (maximum, sum, unnormalised output)
 // in its slot of the workspace, and merge_kernel adds up the partials of the
 // items that were split, in order: the same lengths give the same bits.
@@ -287,8 +287,8 @@ __device__ __forceinline__ float pow2(int e)
 // shares get shorter and 16 x 40000 takes 199 us instead of 176.
 //
 // Measured, 64 query heads over 8 of 128 channels: 16 sequences of 27 to 40
-// thousand positions 167 us, 3.6 TB/s (0.54 of the copy bandwidth); 32 of 2.7 to
-// 4 thousand 49 us.  Issue slots 54 % and ALU 51 % busy at 2.7 warps per
+// thousand positions 166 us, 3.6 TB/s (0.55 of the copy bandwidth); 32 of 2.7 to
+// 4 thousand 47 us.  Issue slots 54 % and ALU 51 % busy at 2.7 warps per
 // scheduler: it is the instructions, some 670 per stage (1000 with values in
 // bf16, scales byte by byte and the maximum by shuffles), that bound it.
 template <int D_, int NT_>
@@ -408,71 +408,17 @@ few_kernel(const Args a)
         const int t_end = min(item_end, (p.unit + count) * kUnit);
         const int32_t *table = a.s.table + int64_t(p.b) * a.s.table_stride;
 
-        // q as the 8-column operand: fp16, a power of two per row
-        uint32_t qf[NT][NB][4];
-        int qexp[NT];                                        // of row 8 nt + g
-        int lim[NT][2], lim_min = 0x7fffffff;                // of rows 8 nt + 2 c, + 1
+        // q, then the first stages on their way before q is used (a small call 9.8 -> 9.0 us); a row that is not
+        // there reads the last one's
+        uint4 raw[NT][NB];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const int r = r0 + 8 * t + g;
-            uint4 raw[NB];
-            uint32_t top = 0;
+            const int r = min(r0 + 8 * t + g, q.rows - 1), token = r / a.group;
+            const __nv_bfloat16 *from =
+                a.q + int64_t(q.lo + token) * a.q_st + int64_t(p.h * a.group + r - token * a.group) * a.q_sh + 8 * c;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                raw[b] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < q.rows)
-                    raw[b] = __ldg(reinterpret_cast<const uint4 *>(a.q + int64_t(q.lo + r / a.group) * a.q_st +
-                                                                   int64_t(p.h * a.group + r % a.group) * a.q_sh +
-                                                                   32 * b + 8 * c));
-                const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {                // the largest finite magnitude: an infinity stays one
-                    const uint32_t lo = (w[i] << 16) & 0x7fff0000u, hi = w[i] & 0x7fff0000u;
-                    top = max(top, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
-                }
-            }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int field = max(int(top >> 23) - 15, 1);
-            const float down = __uint_as_float(uint32_t(254 - field) << 23);
-            qexp[t] = field - 127;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qf[t][b][i] = gemv::pack_f16x2(bf16_lo(w[i]) * down, bf16_hi(w[i]) * down);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int rr = r0 + 8 * t + 2 * c + i;
-                lim[t][i] = rr < q.rows ? row_end(a, q, rr) : 0;
-                if (rr < q.rows) lim_min = min(lim_min, lim[t][i]);
-            }
+            for (int b = 0; b < NB; ++b) raw[t][b] = __ldg(reinterpret_cast<const uint4 *>(from + 32 * b));
         }
-        lim_min = __reduce_min_sync(0xffffffffu, lim_min);
-        int qe[NT][2];                                       // exponents of rows 8 nt + 2 c, + 1
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) qe[t][i] = __shfl_sync(0xffffffffu, qexp[t], 8 * c + 4 * i);
-
-        if (threadIdx.x < 4) nan_first[threadIdx.x] = 0x7fffffff;
-        __syncthreads();
-
-        float m[NT][2], l[NT][2], o[NT][MT][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            m[t][0] = m[t][1] = -INFINITY;
-            l[t][0] = l[t][1] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < MT; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
-        }
-        int vtop = 0, kref = 0;                              // the largest value and key scale bytes so far
-        float cs[NT][2];                                     // what brings S to units of log 2
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) cs[t][i] = a.scale_log2 * pow2(max(qe[t][i] - 127, -126));
         uint32_t on_page = 0;                                // two bits per stage in flight: its strips have a page
 
         const int t_first = p.unit * kUnit + warp * 32;
@@ -515,6 +461,66 @@ few_kernel(const Args a)
             on_page >>= 2;
             fetch(t_first + i * 32 * W, i);
         }
+        // q as the 8-column operand: fp16, a power of two per row
+        uint32_t qf[NT][NB][4];
+        int qexp[NT];                                        // of row 8 nt + g
+        int lim[NT][2], lim_min = 0x7fffffff;                // of rows 8 nt + 2 c, + 1
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int r = r0 + 8 * t + g;
+            uint32_t top = 0;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                if (r >= q.rows) raw[t][b] = make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t w[4] = {raw[t][b].x, raw[t][b].y, raw[t][b].z, raw[t][b].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {                // the largest finite magnitude: an infinity stays one
+                    const uint32_t lo = (w[i] << 16) & 0x7fff0000u, hi = w[i] & 0x7fff0000u;
+                    top = max(top, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
+                }
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int field = max(int(top >> 23) - 15, 1);
+            const float down = __uint_as_float(uint32_t(254 - field) << 23);
+            qexp[t] = field - 127;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const uint32_t w[4] = {raw[t][b].x, raw[t][b].y, raw[t][b].z, raw[t][b].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qf[t][b][i] = gemv::pack_f16x2(bf16_lo(w[i]) * down, bf16_hi(w[i]) * down);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int rr = r0 + 8 * t + 2 * c + i;
+                lim[t][i] = rr < q.rows ? row_end(a, q, rr) : 0;
+                if (rr < q.rows) lim_min = min(lim_min, lim[t][i]);
+            }
+        }
+        lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+        int qe[NT][2];                                       // exponents of rows 8 nt + 2 c, + 1
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) qe[t][i] = __shfl_sync(0xffffffffu, qexp[t], 8 * c + 4 * i);
+
+        if (threadIdx.x < 4) nan_first[threadIdx.x] = 0x7fffffff;
+        __syncthreads();
+
+        float m[NT][2], l[NT][2], o[NT][MT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
+        }
+        int vtop = 0, kref = 0;                              // the largest value and key scale bytes so far
+        float cs[NT][2];                                     // what brings S to units of log 2
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) cs[t][i] = a.scale_log2 * pow2(max(qe[t][i] - 127, -126));
         int it = 0;
         for (int t0 = t_first; t0 < t_end; t0 += 32 * W, ++it) {
             gemv::cp_wait<ST - 2>();

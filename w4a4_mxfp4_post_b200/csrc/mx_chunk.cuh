@@ -41,13 +41,14 @@
 // Every wait is bounded (g_wait_timeouts).
 //
 // Measured, 32 query heads over 8 of 128 channels: 2048 tokens over 32,048
-// positions 0.88 ms, 1.18 PFLOP/s (0.72 of a cuBLAS bf16 product's burst rate,
-// 0.85 of its sustained one); 1024 over 31,000 0.45 ms; a causal prompt of 4096
-// 227 us.  A step of both tiles takes 4050 clocks: tensor pipe and exponential
+// positions 0.86 ms, 1.21 PFLOP/s (0.74 of a cuBLAS bf16 product's burst rate,
+// 0.87 of its sustained one); 512 over 8,512 81 us; a causal prompt of 4096
+// 165 us.  A step of both tiles takes 4050 clocks: tensor pipe and exponential
 // unit 47 % busy, issue slots 49 %.  A tile's turn is Q K' (some 700 clocks with
 // P V before it), the softmax (3000, of which 2000 while the other tile's
-// exponentials compete), then P V.  An item costs some 16,000 clocks beside
-// its steps: queries, the first S, results.
+// exponentials compete), then P V.  An item costs some 12,000 clocks beside
+// its steps: 3,500 until its queries are in place, 1,500 until the first S,
+// 1,300 for the last P V, 4,400 for the results, 1,300 for the next item.
 
 namespace attn {
 namespace chunk {
