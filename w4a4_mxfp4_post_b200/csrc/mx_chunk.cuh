@@ -491,6 +491,14 @@ chunk_kernel(const Args a, long long budget)
         int mine_segs = 0;                   // segments of this tile so far
         const float c = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);
         bool ok = true;
+        // The lane for places in Q and in the results.  With 12 chunks to a row the places cost divisions and would
+        // be kept from item to item, which spills: from a lane that looks new they are worked out again (2 x 777 of
+        // 3000, 96 channels: 92.6 -> 83.4 us; with 16 chunks 55.8 -> 59.3 us, so there they are not).
+        auto fresh_lane = [&] {
+            int ln = lane;
+            if constexpr (NB == 3) asm volatile("" : "+r"(ln));
+            return ln;
+        };
         while (walk.left > 0 && ok) {
             segment();
             const int steps = walk.steps;
@@ -521,15 +529,16 @@ chunk_kernel(const Args a, long long budget)
                     // lanes over the chunks of the warp's rows, so that every load is contiguous, and all loads
                     // before the first use: one after the other they took 13k cycles an item, together 3.5k.  A row
                     // that is not there reads the last one's, for nothing.
+                    const int ln = fresh_lane();
                     uint4 w[D / 8];
 #pragma unroll
                     for (int e = 0; e < D / 8; ++e) {
-                        const int pc = lane + 32 * e, rr = pc / (D / 8), ch = pc % (D / 8);
+                        const int pc = ln + 32 * e, rr = pc / (D / 8), ch = pc % (D / 8);
                         w[e] = __ldg(reinterpret_cast<const uint4 *>(a.q + __shfl_sync(0xffffffffu, from, rr)) + ch);
                     }
 #pragma unroll
                     for (int e = 0; e < D / 8; ++e) {
-                        const int pc = lane + 32 * e, rr = pc / (D / 8), ch = pc % (D / 8), rw = row - lane + rr;
+                        const int pc = ln + 32 * e, rr = pc / (D / 8), ch = pc % (D / 8), rw = row - ln + rr;
                         if (zero)
                             w[e] = make_uint4(hmul2_bf16(w[e].x, 0u), hmul2_bf16(w[e].y, 0u), hmul2_bf16(w[e].z, 0u),
                                               hmul2_bf16(w[e].w, 0u));
@@ -684,6 +693,7 @@ chunk_kernel(const Args a, long long budget)
                 __syncwarp();
                 if (whole) {
                     const int token = r / a.group;
+                    const int ln = fresh_lane();
                     const int64_t to = (int64_t(q.lo + token) * a.hq + p.h * a.group + r - token * a.group) * D;
 #pragma unroll 1
                     for (int e0 = 0; e0 < D / 8; e0 += 4) {
@@ -691,14 +701,14 @@ chunk_kernel(const Args a, long long budget)
                         int64_t at[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int pc = lane + 32 * (e0 + e), rr = pc / (D / 8), ch = pc % (D / 8), rw = row - lane + rr;
+                            const int pc = ln + 32 * (e0 + e), rr = pc / (D / 8), ch = pc % (D / 8), rw = row - ln + rr;
                             w[e] = *reinterpret_cast<const uint4 *>(tile_q + rw * 128 + (ch / 8) * (kTile * 128) + (((ch % 8) ^ (rw & 7)) << 4));
                             at[e] = __shfl_sync(0xffffffffu, to, rr) + 8 * ch;
                         }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int rr = (lane + 32 * (e0 + e)) / (D / 8);
-                            if (r0 + row - lane + rr < q.rows) *reinterpret_cast<uint4 *>(a.out + at[e]) = w[e];
+                            const int rr = (ln + 32 * (e0 + e)) / (D / 8);
+                            if (r0 + row - ln + rr < q.rows) *reinterpret_cast<uint4 *>(a.out + at[e]) = w[e];
                         }
                     }
                     __syncwarp();
