@@ -2956,7 +2956,9 @@ int chunk_launch(const char *fn, const attn::Args &a, cudaStream_t stream)
     return launch_check(fn);
 }
 
-// Rows per kv head from which a sequence goes to the many-rows kernel.
+// Rows per kv head above which a sequence goes to the many-rows kernel.  Few-rows
+// and many-rows kernel, us: 16 sequences of 8000 positions with 40 rows 124 and
+// 128, with 48 132 and 126, with 64 173 and 127; 4 of 1000 with 48 rows 22 and 30.
 constexpr int64_t kChunkRows = 48;
 
 // max_new and T bound a sequence's rows; where there may be many, sequences
