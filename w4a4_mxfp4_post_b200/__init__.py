@@ -720,18 +720,21 @@ def _batch(block_table, cu_seqlens, seq_lens, device):
     try:
         B, pages = block_table.shape
         stride, inner = block_table.stride()
+        if B <= 1:
+            stride = pages                   # (not used, whatever the tensor says)
         if block_table.dtype is i32 and cu_seqlens.dtype is i32 and block_table.device == device \
-                and cu_seqlens.device == device and (inner == 1 or pages <= 1) and cu_seqlens.shape == (B + 1,) \
-                and cu_seqlens.is_contiguous():
+                and cu_seqlens.device == device and stride >= pages and (inner == 1 or pages <= 1) \
+                and cu_seqlens.shape == (B + 1,) and cu_seqlens.is_contiguous():
             if seq_lens is None:
-                return _BATCH.pack(block_table.data_ptr(), max(stride, pages), pages, cu_seqlens.data_ptr(), 0, B), B
+                return _BATCH.pack(block_table.data_ptr(), stride, pages, cu_seqlens.data_ptr(), 0, B), B
             if seq_lens.dtype is i32 and seq_lens.device == device and seq_lens.shape == (B,) and seq_lens.is_contiguous():
-                return _BATCH.pack(block_table.data_ptr(), max(stride, pages), pages, cu_seqlens.data_ptr(),
-                                   seq_lens.data_ptr(), B), B
+                return _BATCH.pack(block_table.data_ptr(), stride, pages, cu_seqlens.data_ptr(), seq_lens.data_ptr(), B), B
     except (AttributeError, TypeError, ValueError):
         pass
     _need_rows(block_table, "block_table", (i32,), 2, device)
-    B = block_table.shape[0]
+    B, pages = block_table.shape
+    if B > 1 and block_table.stride(0) < pages:
+        raise ValueError(f"block_table's rows overlap (stride {block_table.stride(0)}, {pages} entries); make it contiguous")
     _need(cu_seqlens, "cu_seqlens", i32, device, (B + 1,))
     _need(seq_lens, "seq_lens", i32, device, (B,))
     raise ValueError("block_table, cu_seqlens and seq_lens do not fit together")
@@ -743,7 +746,8 @@ def mx_cache_write(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_s
     k, v: bf16 or float32 [T, heads, head_dim], tokens and heads may be strided (slices of a
     fused projection).  The cache: codes uint8 [pages, heads, page_size, head_dim/2] and
     scales uint8 [pages, heads, page_size, head_dim/32] of keys and of values.  Sequences:
-    block_table int32 [B, max_pages], cu_seqlens int32 [B+1] (rows of each sequence),
+    block_table int32 [B, max_pages] (its rows may be strided, but not overlap: an expanded
+    table is refused, .contiguous() does), cu_seqlens int32 [B+1] (rows of each sequence),
     seq_lens int32 [B] (lengths with the new tokens, which are the last ones).
     """
     torch = _torch()

@@ -15,7 +15,6 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
-#include <algorithm>
 #include <array>
 #include <cmath>
 
@@ -81,7 +80,8 @@ bool batch_of(PyObject *const *args, PyObject *lens, const Device &dev, mx_batch
     if (!dev.has(table, at::kInt) || table->dim() != 2 || !(table->size(1) <= 1 || table->stride(1) == 1)) return false;
     b.batch = table->size(0);
     b.max_pages = table->size(1);
-    b.table_stride = std::max(table->stride(0), b.max_pages);
+    b.table_stride = b.batch > 1 ? table->stride(0) : b.max_pages;           // (one row: not used)
+    if (b.table_stride < b.max_pages) return false;                          // rows that overlap
     if (!dev.has(cu, at::kInt) || cu->dim() != 1 || cu->size(0) != b.batch + 1 || !cu->is_contiguous()) return false;
     if (lens && (!dev.has(len, at::kInt) || len->dim() != 1 || len->size(0) != b.batch || !len->is_contiguous())) return false;
     b.block_table = static_cast<const int32_t *>(table->data_ptr());
