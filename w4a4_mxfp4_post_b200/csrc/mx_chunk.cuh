@@ -508,11 +508,9 @@ chunk_kernel(const Args a, long long budget)
             // for both tiles' softmax.
             if (tid < 4) nan_first[(seg + kRing) % kSegs][tid] = 0x7fffffff;
             if (r0 >= walk.q.rows) {
-                // nothing to do, but the next segment begins after both tiles' last, and this tile's arrivals must
-                // not run ahead of the segments
+                // nothing to do, but the next segment begins after both tiles' last
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&qfull[i]);
-                if (!wait(&segdone, seg & 1, budget)) break;
             } else {
                 // positions from the step's first that the row sees; one that is not there sees all, for nothing
                 int lim;
@@ -721,6 +719,9 @@ chunk_kernel(const Args a, long long budget)
                         Desc{int(share_of(end, total, shares)) - int(blockIdx.x) + 1, p.h, p.tile * R, q.lo, q.rows, {}};
                 }
             }
+            // A tile's arrivals must not run ahead of the segments.  Both tiles wait in every segment: a wait on
+            // phase n passes also while phase n - 1 is not complete, so none may be left out.
+            if (!wait(&segdone, seg & 1, budget)) break;
             k += steps;
             advance();
         }
