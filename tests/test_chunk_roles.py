@@ -16,8 +16,7 @@ def softmax_role():
     """Lines of the softmax role's loop over segments, without comments, each with its depth of braces within the loop."""
     with open(SOURCE) as f:
         text = re.sub(r"//[^\n]*", "", f.read())
-    body = text[text.index("setmaxnreg.inc"):]
-    body = body[body.index("while (walk.left > 0 && ok) {"):].split("\n")
+    body = text[text.rindex("while (walk.left > 0 && ok) {"):].split("\n")
     depth, lines = 1, []
     for line in body[1:]:
         if line.strip().startswith("}"):
@@ -106,3 +105,14 @@ def test_every_segment_waits_until_it_is_done():
     waits = [depth for depth, line in lines if "wait(&segdone" in line]
     assert waits == [1], "one wait for segdone, in no branch of the loop over segments"
     assert lines[-1][1] == "advance();"
+
+
+def test_each_warpgroup_has_one_setmaxnreg():
+    """setmaxnreg is for a whole warpgroup: one for warps 0 to 7, all of one role, and one before the roles for the others, which have two."""
+    with open(SOURCE) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    found = [(m.start(), m.group(1)) for m in re.finditer(r"setmaxnreg\.(inc|dec)\.sync\.aligned", text)]
+    assert [kind for _, kind in found] == ["dec", "inc"]
+    roles, softmax = text.index("if (warp >= kSoftmaxWarps && warp < kMmaWarp) {"), text.rindex("} else {", 0, found[1][0])
+    assert re.search(r"if \(warp >= kSoftmaxWarps\) asm volatile\(\"setmaxnreg\.dec", text[:roles])
+    assert text[softmax:found[1][0]].split() == ["}", "else", "{", "asm", 'volatile("']

@@ -63,6 +63,7 @@ constexpr int kMmaWarp = kSoftmaxWarps + kDecodeWarps;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
 // Registers a thread: 128 at launch, some moved to the softmax warpgroups.
 constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;
+static_assert(kSoftmaxWarps % 4 == 0, "the split goes by whole warpgroups");
 static_assert(kThreads == 512 && 256 * (kSoftmaxRegs + kOtherRegs) <= 512 * 128, "the split stays within the launch's registers");
 constexpr int kSegs = 2 * kRing;                             // segments whose NaN positions are kept
 constexpr int kItemCost = 4;                                 // of an item beside its units, in units
@@ -346,9 +347,11 @@ chunk_kernel(const Args a, long long budget)
         __syncwarp();
         ++seg;
     };
+    // All warps of a warpgroup execute the same setmaxnreg: warps 12 to 15 have two roles, so theirs stands before
+    // the roles.  (The softmax warps' there, too, makes their loops spill.)
+    if (warp >= kSoftmaxWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
         // ---------------- keys and values into shared memory
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         int k = 0;                           // steps of the segments so far
         int turn = warp - kSoftmaxWarps;                 // this warp's next task, counted from the segment's first
         bool ok = true;
@@ -407,7 +410,6 @@ chunk_kernel(const Args a, long long budget)
         }
     } else if (warp == kMmaWarp) {
         // ---------------- the MMAs
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         int k = 0, n1 = 0;                   // steps, steps of the second tile so far
         bool ok = true;
         const uint32_t tm = uniform(tmem), aQ = uniform(smem_addr(sQ));
