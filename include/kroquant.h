@@ -351,7 +351,7 @@ int mx_cache_read(const mx_cache *cache, const mx_batch *seqs, const int32_t *st
  *   out[t][h] = softmax_j(scale * q[t][h] . k[j][h / g]) . v[j][h / g]
  * with g = heads_q / heads query heads per kv head, j over the positions up to
  * token t's own (causal != 0) or over all of the sequence's seq_lens[b].
- * q bf16 [T][heads_q][head_dim] with token and head strides (as for
+ * T * g <= 2^31 - 2^10.  q bf16 [T][heads_q][head_dim] with token and head strides (as for
  * mx_cache_write); out bf16 [T][heads_q][head_dim], contiguous.  Scores,
  * maxima and sums in fp32; for the second product the probabilities are
  * rounded to bf16, or (few rows) multiplied by their values' scale and rounded

@@ -1,10 +1,21 @@
 """The few-token operators' binding, without a GPU: what it packs for the library and what it refuses."""
+import ctypes
+
 import pytest
 import torch
 
 import w4a4_mxfp4_post_b200 as kq
 
 CPU = torch.device("cpu")
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def L():
+    from w4a4_mxfp4_post_b200 import build
+
+    build.build()
+    return kq.lib()
 
 
 class Cuda(torch.Tensor):
@@ -39,3 +50,18 @@ def test_block_table_row_strides(lens):
     for shared in (i32(1, 5).expand(4, -1), i32(12).as_strided((3, 5), (3, 1)), i32(8).unfold(0, 5, 1), i32(1, 1).expand(2, -1)):
         with pytest.raises(ValueError, match="overlap"):
             batch_of(shared, lens)
+
+
+def test_attention_rows_end_before_32_bits(L):
+    """The rows of a kv head are counted in 32 bits, to the end of the item behind the last: more are refused, by the size query too."""
+    cache, seqs = kq._CACHE.pack(16, 16, 16, 16, 4, 2, 16, 64), kq._BATCH.pack(16, 3, 3, 16, 16, 2)
+    most = (1 << 31) - (1 << 10)
+    for T, hq in (((1 << 31) - 1, 2), (most + 1, 2), (most // 2 + 1, 4)):
+        assert L.mx_paged_attention(P(16), 256, 64, cache, seqs, 1.0, 1, P(16), T, hq, 1, P(16), 1 << 62, None) == -2
+        assert "2^31 - 2^10" in L.kq_last_error().decode()
+        assert L.mx_attention_workspace(T, hq, 2, 64, 1) == -1
+    # (the last that is taken fails the next check)
+    assert L.mx_paged_attention(None, 256, 64, cache, seqs, 1.0, 1, P(16), most, 2, 1, P(16), 1 << 62, None) == -1
+    assert L.mx_attention_workspace(most, 2, 2, 64, 1) > 0
+    for bad in ((1 << 31, 2, 2, 64, 0), (1 << 62, 1 << 62, 2, 64, 1), (4, 1 << 40, 2, 64, 1), (4, 1 << 17, 1 << 17, 64, 1)):
+        assert L.mx_attention_workspace(*bad) == -1

@@ -2684,6 +2684,10 @@ bool head_dim_ok(int64_t D) { return D == 32 || D == 64 || D == 96 || D == 128; 
 // Positions of a sequence: a few stages past the last one still fit 32 bits.
 constexpr int64_t kMaxPositions = (int64_t(1) << 31) - (1 << 20);
 
+// Rows per kv head of a call (tokens x query heads per kv head): the end of the
+// item behind the last one still fits 32 bits.
+constexpr int64_t kMaxAttnRows = (int64_t(1) << 31) - (1 << 10);
+
 // Checks of a cache and a batch that need no pointer; fills `s`.
 int check_seqs(const char *fn, const mx_cache *c, const mx_batch *b, int64_t T, cache::Seqs *s)
 {
@@ -3459,7 +3463,9 @@ int mx_cache_read(const mx_cache *c, const mx_batch *b, const int32_t *starts, v
 
 int64_t mx_attention_workspace(int64_t T, int64_t heads_q, int64_t heads, int64_t head_dim, int64_t max_new)
 {
-    if (T < 0 || heads < 1 || heads_q < 1 || heads_q % heads != 0 || !head_dim_ok(head_dim) || max_new < 0) return -1;
+    if (T < 0 || T >= (int64_t(1) << 31) || heads < 1 || heads > 65535 || heads_q < 1 || heads_q % heads != 0 ||
+        heads_q > 65535 * heads || T * (heads_q / heads) > kMaxAttnRows || !head_dim_ok(head_dim) || max_new < 0)
+        return -1;
     const int64_t most = max_new < T ? max_new : T;
     const int64_t slots = most * (heads_q / heads) > kChunkRows ? 2 * attn::chunk::kMaxCtas * attn::chunk::R
                                                                 : 2 * attn::kMaxCtas * 16;
@@ -3478,8 +3484,8 @@ int mx_paged_attention(const void *q_bf16, int64_t q_stride_t, int64_t q_stride_
         return fail(KQ_ERR_SHAPE, "%s: heads_q must be a positive multiple of the cache's heads (%lld, %lld)", fn,
                     (long long)heads_q, (long long)c->heads);
     if (max_new < 0) return fail(KQ_ERR_SHAPE, "%s: max_new must not be negative", fn);
-    if (T * (heads_q / c->heads) >= (int64_t(1) << 31))
-        return fail(KQ_ERR_SHAPE, "%s: T * heads_q / heads must be below 2^31 (T=%lld)", fn, (long long)T);
+    if (T * (heads_q / c->heads) > kMaxAttnRows)
+        return fail(KQ_ERR_SHAPE, "%s: T * heads_q / heads must be at most 2^31 - 2^10 (T=%lld)", fn, (long long)T);
     const float scale_log2 = scale * 1.44269504088896340736f;    // scores in units of log 2
     if (!std::isfinite(scale_log2)) return fail(KQ_ERR_SHAPE, "%s: scale must be finite, also times log2(e)", fn);
     if (T == 0 || b->batch == 0) return ok();
