@@ -7,7 +7,7 @@ import torch
 
 import serve_ref as ref
 import w4a4_mxfp4_post_b200 as kq
-from test_gpu_serve import Plan, attend, normal
+from test_gpu_serve import Plan, attend, normal, operand, rng
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,46 @@ def test_a_single_sequence_with_any_row_stride(cuda_device, either_binding):
     for stride in (0, 1, 1000):
         p.table = p.table.as_strided(p.table.shape, (stride, 1))
         assert torch.equal(attend(p, q, max_new=3), want)
+
+
+# --- products ----------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [1, 7, 12, 20])
+@pytest.mark.parametrize("lo,hi", [(220, 227), (231, 241), (248, 255)])
+def test_gemv_scales_up_to_the_largest(cuda_device, M, lo, hi):
+    """Scales up to 2^127, beside the smallest ones in the same tile of weights, over rows of x of unlike sizes: every product
+    whose terms fp32 holds comes out within its bound, with no infinity or NaN on the way."""
+    N, K = 200, 1120
+    c, s = operand(N, K, lo, lo, hi)
+    g = rng(M, lo)
+    small = torch.randint(0, 40, s.shape, dtype=torch.uint8, device="cuda", generator=g)
+    kind = torch.arange(N, device="cuda") % 3
+    s = torch.where(kind[:, None] == 0, small, s)            # all small, all large, and both within a row
+    mixed = (kind[:, None] == 2) & (torch.rand(s.shape, device="cuda", generator=g) < 0.5)
+    s = torch.where(mixed, small, s)
+    gain = 2.0 ** torch.tensor([-(hi - 127) - 1 + 110, -(hi - 127) + 90, -90, 0, 20], device="cuda").float()
+    x = (normal(M, K, key=lo).float() * gain[torch.arange(M, device="cuda") % 5][:, None]).bfloat16()
+    y, ab, tail = ref.gemv(x, c, s)
+    out = kq.mxf4_gemv(x, c, ref.sf_of(s), out_dtype=torch.float32)
+    held = ab < 2.0 ** 126
+    assert held.sum() > M * N // 4 and ((s >= 224).any(1)[None] & held & (ab > 2.0 ** 60)).any()
+    # (2^-126: a rounding below fp32's normal numbers, as in test_gpu_serve.py)
+    tol = ref.gemv_bound(y, ab, tail, K, False) + 2.0 ** -126
+    assert ((out.double() - y).abs() <= tol)[held].all()
+
+
+@pytest.mark.parametrize("M", [1, 20])
+def test_gemv_of_one_and_a_large_weight(cuda_device, M):
+    """x = 1 times a weight of 2^113 is 2^113."""
+    N, K = 40, 256
+    c = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
+    c[:, 5] = 2
+    s = torch.full((N, K // 32), 127, dtype=torch.uint8, device="cuda")
+    s[:, 0] = 240
+    x = torch.ones(M, K, dtype=torch.bfloat16, device="cuda")
+    assert (kq.mxf4_gemv(x, c, ref.sf_of(s)) == 2.0 ** 113).all()
+    s[7, 0], s[9, 1] = 255, 255
+    out = kq.mxf4_gemv(x, c, ref.sf_of(s))
+    nan = torch.zeros(N, dtype=torch.bool, device="cuda")
+    nan[[7, 9]] = True
+    assert out[:, nan].isnan().all() and (out[:, ~nan] == 2.0 ** 113).all()

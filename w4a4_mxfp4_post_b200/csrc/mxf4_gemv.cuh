@@ -23,7 +23,7 @@
 // where x' = x 2^-ex is a chunk (256 channels) of x brought to fp16 by a power
 // of two that puts its largest element in [2^15, 2^16): bf16's 8 bits stay
 // exact down to 2^-32 of the largest; what is below is off by at most 2^-40 of
-// it, half the step of fp16's subnormals.
+// it, half the step of fp16's subnormals.  (Where a scale is 2^97 or more, 2^ex comes first.)
 //
 // Layout.  A warp owns a tile of 16 weight rows: 4 consecutive lanes l of a
 // 128-row scale group and their 4 quarters (rows base + 32 q + l), so that its
@@ -290,12 +290,15 @@ mxf4_gemv_kernel(const __nv_bfloat16 *__restrict__ x, int64_t ldx, const uint8_t
 
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) fetch(c0 + i * KG + kg, i);
+    const bool row_there = group * 128 + (lane & 3) * 32 + l0 + ((lane >> 2) & 3) < N;    // of this lane's scale bytes
     // chunk ch of the stage at `st` times x at `xc` with the exponents `ex`
     auto product = [&](int ch, const uint8_t *st, const uint8_t *xc, const float *ex) {
+        bool large;                                           // some scale is 2^97 or more (or NaN)
         {
             // the stage's 128 scales as floats, [unit][row][4]: lane = unit * 16 + (l * 4 + quarter)
             const uint32_t w = reinterpret_cast<const uint32_t *>(st + kCodeBytes)[lane];
             float4 s = scales4(w);
+            large = __any_sync(0xffffffffu, row_there && (w & (w << 1) & (w << 2) & 0x80808080u) != 0);
             const int left = nb - (ch * kChunkBlocks + (lane / 16) * 4);
             if (left < 4) {                               // padding bytes of the last unit may hold anything
                 if (left < 1) s.x = 0.0f;
@@ -307,6 +310,34 @@ mxf4_gemv_kernel(const __nv_bfloat16 *__restrict__ x, int64_t ldx, const uint8_t
         }
         __syncwarp();
         xc += g * 64 + c * 16;
+        if (large) {
+            // x' carries up to 2^16 and a block's sum 2^24: times such a scale that may pass fp32's range although the
+            // product does not.  The exponent of x is applied first then, block by block (last where the scale is
+            // below 1, for the same reason).  Rare: not unrolled.
+#pragma unroll 1
+            for (int j = 0; j < kChunkBlocks; ++j) {
+                const uint8_t *row = st + g * 128 + ((j ^ g) << 4) + c * 4;
+                const float *scale = reinterpret_cast<const float *>(table + (j / 4) * 16 + g) + j % 4;
+                const float lo = scale[0], hi = scale[8 * 4];
+                uint32_t a[4], d[4];
+                codes_f16(*reinterpret_cast<const uint32_t *>(row), a);
+                codes_f16(*reinterpret_cast<const uint32_t *>(row + 8 * 128), d);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint4 bx = *reinterpret_cast<const uint4 *>(xc + j * kXBlockBytes<NT> + t * 512);
+                    const float2 e = *reinterpret_cast<const float2 *>(ex + 8 * t + 2 * c);
+                    float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma_f16(p, a[0], d[0], a[1], d[1], bx.x, bx.y);
+                    mma_f16(p, a[2], d[2], a[3], d[3], bx.z, bx.w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float f = i < 2 ? lo : hi, ei = i % 2 ? e.y : e.x;
+                        acc[t][i] = f >= 1.0f ? fmaf(p[i] * ei, f, acc[t][i]) : fmaf(p[i] * f, ei, acc[t][i]);
+                    }
+                }
+            }
+            return;
+        }
         float sum[NT][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
