@@ -89,3 +89,24 @@ def test_gemv_of_one_and_a_large_weight(cuda_device, M):
     nan = torch.zeros(N, dtype=torch.bool, device="cuda")
     nan[[7, 9]] = True
     assert out[:, nan].isnan().all() and (out[:, ~nan] == 2.0 ** 113).all()
+
+
+# --- attention ---------------------------------------------------------------
+
+# a few rows (groups of 4 and 12: both widths); items that one CTA holds, and items that are split
+LARGE = [([0], [1], 4), ([150], [1], 12), ([700, 90], [2, 1], 4), ([20000], [1], 4), ([9000, 12000], [3, 1], 4)]
+
+
+def large_values(past, new, group, lo, hi, codes=None):
+    p = Plan(past, new, 2, 64, 32, seed=lo)
+    p.vs.copy_(torch.randint(lo, hi, p.vs.shape, dtype=torch.uint8, device="cuda", generator=rng(lo, hi)))
+    if codes is not None:
+        p.vc.fill_(codes)
+    attend(p, normal(p.T, 2 * group, 64, key=lo), max_new=max(new))
+
+
+@pytest.mark.parametrize("lo,hi,codes", [(225, 227, 0x77), (238, 246, None), (200, 253, None), (252, 253, 0x77), (252, 253, 0xF7)])
+@pytest.mark.parametrize("past,new,group", LARGE)
+def test_attention_values_up_to_the_largest(cuda_device, past, new, group, lo, hi, codes):
+    """Sums over many positions of the largest values are past fp32, their mean is not."""
+    large_values(past, new, group, lo, hi, codes)

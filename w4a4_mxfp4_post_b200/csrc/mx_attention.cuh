@@ -19,9 +19,11 @@
 // long sequences split over as many CTAs as they need.  (What an item costs beside
 // its units counts as units, too: a causal prompt of 4096, whose first items are
 // one unit long, took 253 us without, 165 with.)  A CTA whose share ends inside
-// an item leaves a partial result (maximum, sum, unnormalised output)
+// an item leaves a partial result (maximum, sum, output of its positions alone)
 // in its slot of the workspace, and merge_kernel adds up the partials of the
 // items that were split, in order: the same lengths give the same bits.
+// (Partial outputs are weighted means, as the result: sums over many positions of
+// values near the end of the format's range are past that of fp32.)
 
 namespace attn {
 
@@ -53,8 +55,8 @@ struct Desc {
     int pad[3];
 };
 
-// Slot i of a workspace for R rows: unnormalised output [D / 4][R][4] (a thread
-// per row writes whole lines), maxima [R], sums [R].
+// Slot i of a workspace for R rows: output [D / 4][R][4] (a thread per row writes
+// whole lines), maxima [R], sums [R].
 template <int R, int D>
 __device__ __forceinline__ float *slot(const Args &a, int i)
 {
@@ -370,9 +372,11 @@ few_kernel(const Args a)
 {
     pdl_wait();
     constexpr int D = C::D, NT = C::NT, R = C::R, NB = C::NB, MT = C::MT, W = C::kWarps, ST = C::kStages;
-    extern __shared__ __align__(16) uint8_t smem_dyn[];
+    // (aligned to whole 32-byte sectors at least: on 16 bytes 16 x 40000 takes 8 % longer)
+    extern __shared__ __align__(128) uint8_t smem_few[];
     __shared__ int64_t sh[W * 32 + 34];
     __shared__ int nan_first[4];             // per 32 channels: the first position of the item whose value is NaN
+    __shared__ int vtops[W];                 // the warps' largest value scales
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
 
     Place p;
@@ -383,7 +387,7 @@ few_kernel(const Args a)
     if (threadIdx.x == 0) desc->parts = 0;
     if (left <= 0) return;
 
-    uint8_t *ring = smem_dyn + warp * C::kWarpBytes;
+    uint8_t *ring = smem_few + warp * C::kWarpBytes;
     float *ktab = reinterpret_cast<float *>(ring + ST * C::kStage);          // [32 positions][4]
     uint32_t *vtab = reinterpret_cast<uint32_t *>(ktab + 128);               // [16 pairs][4]
     const uint32_t ring_s = smem_addr(ring);
@@ -786,10 +790,16 @@ few_kernel(const Args a)
         }
         gemv::cp_wait<0>();
 
-        // ---- the warps' results together: output [W][R][D], maxima and sums [W][R]
+        // ---- the warps' results together: output [W][R][D], maxima and sums [W][R].  Outputs stay relative to the
+        // largest value scale until they are divided by the sum: 2^15 times a sum of many of the largest values is
+        // past fp32.
+        if (lane == 0) vtops[warp] = vtop;
         __syncthreads();
-        float *ow = reinterpret_cast<float *>(smem_dyn), *mw = ow + W * R * C::kOutRow, *lw = mw + W * R;
-        const float vs = pow2(vtop - 127);
+        float *ow = reinterpret_cast<float *>(smem_few), *mw = ow + W * R * C::kOutRow, *lw = mw + W * R;
+        int vmax = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) vmax = max(vmax, vtops[w]);
+        const float vs = pow2(vtop - vmax), vscale = pow2(vmax - 126);       // (half of it is in `inv`)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -830,12 +840,14 @@ few_kernel(const Args a)
                 x = fmaf(v.x, f, x);
                 y = fmaf(v.y, f, y);
             }
+            // (a row that has seen nothing has zeros: they stay)
+            const float inv = ll == 0.0f ? 0.5f : 0.5f / ll;
+            x = x * inv * vscale;
+            y = y * inv * vscale;
             if (nan_first[d / 32] < row_end(a, q, row)) x = y = __uint_as_float(0x7fc00000u);
             if (whole) {
-                const float inv = 1.0f / ll;
-                const uint32_t v = ll == 0.0f && x == 0.0f ? 0u : mma::pack_bf16x2(x * inv, y * inv);
                 *reinterpret_cast<uint32_t *>(a.out + (int64_t(q.lo + row / a.group) * a.hq + p.h * a.group + row % a.group) * D +
-                                              d) = v;
+                                              d) = mma::pack_bf16x2(x, y);
             } else {
                 *reinterpret_cast<float2 *>(sl + slot_at<R>(r, d)) = make_float2(x, y);
                 if (d == 0) {
@@ -863,8 +875,7 @@ __global__ void __launch_bounds__(THREADS)
 merge_kernel(const Args a)
 {
     pdl_wait();
-    __shared__ float weight[ROWS][kMaxCtas];                   // of each part
-    __shared__ float sums[ROWS];
+    __shared__ float weight[ROWS][kMaxCtas];                   // of each part: its share of the sum
     const int share = int(blockIdx.x) / (R / ROWS), first = int(blockIdx.x) % (R / ROWS) * ROWS;
     const Desc d = reinterpret_cast<const Desc *>(a.work)[share];
     if (d.parts == 0) return;
@@ -899,13 +910,14 @@ merge_kernel(const Args a)
         for (int k = lane; k < d.parts; k += 32) {
             const float mk = weight[r][k], lk = k == lane ? lk_first : part(k)[R * D + R + first + r];
             // a part that saw nothing has nothing; a NaN sum reaches the result
-            const float f = mk == -INFINITY ? (lk == 0.0f ? 0.0f : lk) : ex2(mk - mm);
+            const float f = mk == -INFINITY ? (lk == 0.0f ? 0.0f : lk) : lk * ex2(mk - mm);
             weight[r][k] = f;
-            ll = fmaf(lk, f, ll);
+            ll += f;
         }
 #pragma unroll
         for (int i = 16; i; i >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, i);
-        if (lane == 0) sums[r] = ll;
+        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+        for (int k = lane; k < d.parts; k += 32) weight[r][k] *= inv;
     }
     __syncthreads();
     if (mine) {
@@ -934,10 +946,8 @@ merge_kernel(const Args a)
             x.z += v.z;
             x.w += v.w;
         }
-        const float ll = sums[r], inv = 1.0f / ll;
-        const uint2 v = ll == 0.0f && x.x == 0.0f ? make_uint2(0u, 0u)
-                                                  : make_uint2(mma::pack_bf16x2(x.x * inv, x.y * inv), mma::pack_bf16x2(x.z * inv, x.w * inv));
-        *reinterpret_cast<uint2 *>(a.out + (int64_t(d.lo + row / a.group) * a.hq + d.h * a.group + row % a.group) * D + 4 * ch) = v;
+        *reinterpret_cast<uint2 *>(a.out + (int64_t(d.lo + row / a.group) * a.hq + d.h * a.group + row % a.group) * D + 4 * ch) =
+            make_uint2(mma::pack_bf16x2(x.x, x.y), mma::pack_bf16x2(x.z, x.w));
     }
 }
 
