@@ -110,3 +110,27 @@ def large_values(past, new, group, lo, hi, codes=None):
 def test_attention_values_up_to_the_largest(cuda_device, past, new, group, lo, hi, codes):
     """Sums over many positions of the largest values are past fp32, their mean is not."""
     large_values(past, new, group, lo, hi, codes)
+
+
+# many rows: one tile and two, whole items and split ones, beside a single token's sequence
+LARGE_CHUNKS = [([150], [64], 2), ([0], [300], 4), ([9000], [100], 4), ([2500, 500, 40], [90, 130, 1], 4)]
+
+
+@pytest.mark.parametrize("lo,hi,codes", [(205, 211, None), (225, 227, 0x77), (238, 246, None), (200, 253, None), (252, 253, 0x77), (252, 253, 0xF7)])
+@pytest.mark.parametrize("past,new,group", LARGE_CHUNKS)
+def test_chunk_values_up_to_the_largest(cuda_device, past, new, group, lo, hi, codes):
+    large_values(past, new, group, lo, hi, codes)
+    assert kq.kq_wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("past", [0, 130, 3000])
+def test_a_large_value_changes_nothing_for_who_does_not_see_it(cuda_device, past):
+    """One token of a chunk has values near the end of the range: the rows before it keep their bits, those after it are right."""
+    new, at = 150, 70
+    p = Plan([past], [new], 2, 64, 32, seed=past)
+    q = normal(new, 8, 64, key=past)
+    base = attend(p, q, max_new=new)
+    pos = past + at
+    p.vs[int(p.table[0, pos // 32]), :, pos % 32] = 250
+    out = attend(p, q, max_new=new)
+    assert torch.equal(out[:at], base[:at]) and not torch.equal(out[at:], base[at:])

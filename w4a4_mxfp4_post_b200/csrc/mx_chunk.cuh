@@ -70,6 +70,12 @@ constexpr int kItemCost = 4;                                 // of an item besid
 constexpr int kMergeQuads = 8;                               // channels / 4 that a CTA of the merge takes
 constexpr int kMaxCtas = 192;                                // shares
 constexpr float kSlack = 8.0f;                               // log2 of how far a maximum may be stale
+// Values are summed at their full size, so sums over many large ones would pass fp32's range.  From this scale byte on
+// (two bits in a byte) the probabilities of the rows that see one are taken 2^-48 smaller: below it 2^kSlack times 2^31
+// values of 6 x 2^64 are still finite, from it on 2^31 of the largest; what gets lost is below 2^-78 of a row's largest
+// probability or 2^-166 of the largest value.
+constexpr uint32_t kLargeByte = 192;
+constexpr float kLower = 48.0f;
 constexpr uint32_t kO = 256;                                 // tensor memory: S of tile i at 128 i, O at 256 + 128 i
 static_assert(kStep == kTile && kStep == kUnit, "S is square, a step is a unit");
 
@@ -165,8 +171,20 @@ template <int NB>
 struct Piece {
     uint4 c[NB];
     uint32_t s;                              // scale bytes
+    uint32_t vs;                             // with keys: scale bytes of the values (load_vscales)
     bool on;                                 // within the segment and on a page
 };
+
+// Scale bytes of the values beside 32 keys (positions t .. t + 31, a position's pool row in each lane): two strips of
+// 16 NB contiguous bytes, a word to each of the first 8 NB lanes.
+template <int NB>
+__device__ __forceinline__ uint32_t load_vscales(const uint8_t *__restrict__ scales, int64_t row)
+{
+    if constexpr (NB == 4) return row >= 0 ? __ldg(reinterpret_cast<const uint32_t *>(scales) + row) : 0u;
+    const int lane = threadIdx.x % 32;
+    const int64_t first = __shfl_sync(0xffffffffu, row, lane < 4 * NB ? 0 : 16);
+    return lane < 8 * NB && first >= 0 ? __ldg(reinterpret_cast<const uint32_t *>(scales + first * NB) + lane % (4 * NB)) : 0u;
+}
 
 template <int NB>
 __device__ __forceinline__ void load_piece(Piece<NB> &p, const uint8_t *__restrict__ codes,
@@ -259,6 +277,8 @@ chunk_kernel(const Args a, long long budget)
     __shared__ uint32_t tmem_slot;
     __shared__ __align__(16) uint32_t visible[4][4];         // of step s % 4: the positions that are on a page, 32 to a word
     __shared__ int nan_first[kSegs][4];      // of segment i % kSegs, per 32 channels: the first position whose value is NaN
+    __shared__ int large_first[kSegs];       // and the first with a large value
+    __shared__ uint32_t lowered[kSoftmaxWarps];              // rows of a warp whose probabilities are taken smaller
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = base, *sK = base + 2 * C::kQBytes, *sV = sK + kRing * C::kStepBytes;
     __shared__ uint64_t kfull[kRing], kempty[kRing], vfull[kRing], vempty[kRing];
@@ -307,6 +327,7 @@ chunk_kernel(const Args a, long long budget)
         }
     }
     if (tid < kSegs * 4) nan_first[tid / 4][tid % 4] = 0x7fffffff;
+    if (tid < kSegs) large_first[tid] = 0x7fffffff;
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_slot)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -375,6 +396,7 @@ chunk_kernel(const Args a, long long budget)
                 if (page >= 0 && page < a.s.num_pages)
                     row = (int64_t(page) * a.s.heads + head) * a.s.page + (t - page_index(t) * a.s.page);
                 load_piece<NB>(v, is_v ? a.vc : a.kc, is_v ? a.vs : a.ks, row);
+                if (!is_v) v.vs = load_vscales<NB>(a.vs, row);
             };
             Piece<NB> next;
             load(next, turn, page_of(turn));
@@ -398,6 +420,15 @@ chunk_kernel(const Args a, long long budget)
                 } else {
                     const uint32_t on = __ballot_sync(0xffffffffu, cur.on);
                     if (lane == 0) visible[ku & 3][part] = on;
+                    // the values' scales with the keys, for the softmax has to know before it makes probabilities
+                    if (cur.vs & (cur.vs << 1) & 0x80808080u) {
+#pragma unroll 1
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t sb = (cur.vs >> (8 * e)) & 0xffu;
+                            const int t = t_first + u * kStep + 32 * part + 16 * (lane / (4 * NB)) + (4 * (lane % (4 * NB)) + e) / NB;
+                            if (sb >= kLargeByte && sb < kNanByte && t < t_end) atomicMin(&large_first[seg % kSegs], t);
+                        }
+                    }
                 }
                 decode_row<NB>(cur, smem_addr(is_v ? sV : sK) + st * C::kStepBytes, row, !is_v);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -505,10 +536,12 @@ chunk_kernel(const Args a, long long budget)
             segment();
             const int steps = walk.steps;
             const int r0 = walk.p.tile * R + i * kTile;
-            // The values run kRing steps, so at most kRing segments ahead: nobody writes this slot before this
+            // Keys and values run kRing steps, so at most kRing segments ahead: nobody writes this slot before this
             // segment's P V, and who read it (kRing segments ago) is through, since a segment's first MMA waits
             // for both tiles' softmax.
             if (tid < 4) nan_first[(seg + kRing) % kSegs][tid] = 0x7fffffff;
+            if (tid == 0) large_first[(seg + kRing) % kSegs] = 0x7fffffff;
+            if (lane == 0) lowered[warp] = 0;
             if (r0 >= walk.q.rows) {
                 // nothing to do, but the next segment begins after both tiles' last
                 __syncwarp();
@@ -595,9 +628,20 @@ chunk_kernel(const Args a, long long budget)
                     maximum(tS + 64);
                     top = fmaxf(top, top2);
                     const bool grown = top != m && (top - m) * c > kSlack;
-                    if (__any_sync(0xffffffffu, grown)) {
-                        const float al = !grown ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - top) * c);
+                    // (this step's keys have been decoded, so its large values are known)
+                    const int large = *const_cast<volatile int *>(&large_first[seg % kSegs]);
+                    float lower = 0.0f;
+                    if (__any_sync(0xffffffffu, grown || large != 0x7fffffff)) {
+                        float al = !grown ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - top) * c);
                         if (grown) m = top;
+                        if (large != 0x7fffffff) {           // rarest: rows that see it, from now on or before
+                            const bool sees = large - (walk.t_first + u * kStep) < lim;
+                            if (sees) lower = kLower;
+                            if (sees && !((lowered[warp] >> lane) & 1)) al *= ex2(-kLower);
+                            const uint32_t now = __ballot_sync(0xffffffffu, sees);
+                            if (lane == 0) lowered[warp] = now;
+                            __syncwarp();
+                        }
                         l *= al;
                         if (u > 0) {
 #pragma unroll 1
@@ -613,7 +657,7 @@ chunk_kernel(const Args a, long long budget)
                         }
                     }
                     // a row that has seen nothing has the maximum -infinity: its probabilities are zeros
-                    const float mc = m == -INFINITY ? 0.0f : m * c;
+                    const float mc = m == -INFINITY ? 0.0f : fmaf(m, c, lower);
                     float2 sum0 = make_float2(l, 0.0f), sum1 = make_float2(0.0f, 0.0f);
                     auto probs = [&](const float (&v)[32], uint32_t dst) {
                         uint32_t w[16];
@@ -661,9 +705,10 @@ chunk_kernel(const Args a, long long budget)
                 float *sl = slot<R, D>(a, 2 * int(blockIdx.x) + (p.unit == 0 ? 1 : 0));
                 const int ir = i * kTile + row;                              // row of the item
                 // a row that has seen nothing has zeros (or NaN) in O: they stay
-                const float scale = !whole || l == 0.0f ? 1.0f : 1.0f / l;
+                const float scale = l == 0.0f ? 1.0f : 1.0f / l;
                 if (!whole && mine) {
-                    sl[R * D + ir] = m == -INFINITY ? m : m * c;
+                    const float lower = (lowered[warp] >> lane) & 1 ? kLower : 0.0f;
+                    sl[R * D + ir] = m == -INFINITY ? m : fmaf(m, c, lower);
                     sl[R * D + R + ir] = l;
                 }
 #pragma unroll 1
@@ -760,14 +805,18 @@ merge_many_kernel(const Args a)
     load(v1, 1);
     float mm = -INFINITY, ll = 0.0f;
     for (int k = 0; k < d.parts; ++k) mm = fmaxf(mm, part(k)[R * D + r]);
+    auto weight = [&](int k) {
+        const float mk = part(k)[R * D + r], lk = part(k)[R * D + R + r];
+        // a part that saw nothing has nothing; a NaN sum reaches the result
+        return mk == -INFINITY ? (lk == 0.0f ? 0.0f : lk) : lk * ex2(mk - mm);
+    };
+    for (int k = 0; k < d.parts; ++k) ll += weight(k);
+    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
     float4 x[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int k = 0; k < d.parts; ++k) {
-        const float mk = part(k)[R * D + r], lk = part(k)[R * D + R + r];
-        // a part that saw nothing has nothing; a NaN sum reaches the result
-        const float f = mk == -INFINITY ? (lk == 0.0f ? 0.0f : lk) : ex2(mk - mm);
-        ll = fmaf(lk, f, ll);
+        const float f = weight(k) * inv;                     // its share of the sum
         float4 v[kPer];
         if (k > 1) load(v, k);
 #pragma unroll
@@ -779,16 +828,13 @@ merge_many_kernel(const Args a)
             x[j].w = fmaf(u.w, f, x[j].w);
         }
     }
-    const float inv = 1.0f / ll;
     const int row = d.r0 + r, token = row / a.group;
     __nv_bfloat16 *out = a.out + (int64_t(d.lo + token) * a.hq + d.h * a.group + row - token * a.group) * D + 4 * quad;
 #pragma unroll
     for (int j = 0; j < kPer; j += 2) {
-        auto pair = [&](float u, float w) {
-            return mma::pack_bf16x2(ll == 0.0f && u == 0.0f ? 0.0f : u * inv, ll == 0.0f && w == 0.0f ? 0.0f : w * inv);
-        };
-        *reinterpret_cast<uint4 *>(out + 4 * j) = make_uint4(pair(x[j].x, x[j].y), pair(x[j].z, x[j].w),
-                                                             pair(x[j + 1].x, x[j + 1].y), pair(x[j + 1].z, x[j + 1].w));
+        *reinterpret_cast<uint4 *>(out + 4 * j) =
+            make_uint4(mma::pack_bf16x2(x[j].x, x[j].y), mma::pack_bf16x2(x[j].z, x[j].w),
+                       mma::pack_bf16x2(x[j + 1].x, x[j + 1].y), mma::pack_bf16x2(x[j + 1].z, x[j + 1].w));
     }
 }
 
