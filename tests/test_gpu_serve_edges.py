@@ -134,3 +134,22 @@ def test_a_large_value_changes_nothing_for_who_does_not_see_it(cuda_device, past
     p.vs[int(p.table[0, pos // 32]), :, pos % 32] = 250
     out = attend(p, q, max_new=new)
     assert torch.equal(out[:at], base[:at]) and not torch.equal(out[at:], base[at:])
+
+
+@pytest.mark.parametrize("top", [1, 13, 15, 16, 20, 25])
+@pytest.mark.parametrize("past,new,group", [([0], [1], 4), ([150], [1], 12), ([9000], [1], 4), ([150], [64], 2), ([3000], [130], 4)])
+def test_attention_values_of_the_smallest_scale(cuda_device, past, new, group, top):
+    """Values of scale byte 0 (2^-127) beside zeros of larger scale bytes: 6 x 2^-127 is a normal number of bf16."""
+    p = Plan(past, new, 2, 64, 32, seed=top)
+    p.vc.fill_(0x77)
+    p.vs.zero_()
+    pos = torch.arange(0, p.lens[0], 3, device="cuda")
+    pg, at = p.table[0][pos // 32].long(), pos % 32
+    if past != [0]:
+        p.vs[pg, :, at], p.vc[pg, :, at] = top, 0
+    q = normal(p.T, 2 * group, 64, key=top)
+    got = kq.mx_paged_attention(q, *p.args, max_new=max(new)).double()
+    want, tol = ref.attention(q, p.cache, p.table, p.cu, p.lens, 64 ** -0.5, True)
+    # where the weight of the zeros leaves less than 2^-126, bf16's steps are 2^-133 whatever the value: half a step of that
+    assert ((got - want).abs() <= tol + 2.0 ** -134).all()
+    assert (got != 0).any()

@@ -600,11 +600,14 @@ few_kernel(const Args a)
                     }
                 }
             }
-            // a block with 0 < scale < vtop - kWindow: bit 8 of (scale + 255), and not of scale + 256 - the limit
+            // a block with 0 < scale < vtop - kWindow: bit 8 of (scale + 255), and not of scale + 256 - the limit.  Scale
+            // 0 is a block of zeros' (it counts for nothing in fp16) or 2^-127, which counts while that is not below
+            // 2^-40 of the largest: up to 55.
             bool wide;
             {
                 const uint32_t limit = uint32_t(256 - max(vtop - kWindow, 0)) * 0x00010001u;
-                const uint32_t low = ((v2[0] + 0x00ff00ffu) & ~(v2[0] + limit)) | ((v2[1] + 0x00ff00ffu) & ~(v2[1] + limit));
+                const uint32_t some = vtop < 56 ? 0x01000100u : 0x00ff00ffu;
+                const uint32_t low = ((v2[0] + some) & ~(v2[0] + limit)) | ((v2[1] + some) & ~(v2[1] + limit));
                 wide = __any_sync(0xffffffffu, (low & 0x01000100u) != 0);
             }
             {
