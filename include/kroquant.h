@@ -356,7 +356,7 @@ int mx_cache_read(const mx_cache *cache, const mx_batch *seqs, const int32_t *st
  * maxima and sums in fp32; for the second product the probabilities are
  * rounded to bf16, or (few rows) multiplied by their values' scale and rounded
  * to fp16: half a step of it, or 2^-40 of the largest value scale times 6.  A position on no page is not seen; a row that sees nothing is
- * zero; what a row does not see does not reach it, NaN or not.  K and V scale
+ * zero (one whose every score is -infinity NaN, as the formula has it); what a row does not see does not reach it, NaN or not.  K and V scale
  * bytes 253 to 255 (mx_cache_write writes none of the first two) read as NaN.
  * max_new: a bound on the new tokens of any one sequence (T does); it selects
  * the kernels and changes no result beyond rounding.  workspace:

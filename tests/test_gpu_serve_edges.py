@@ -153,3 +153,41 @@ def test_attention_values_of_the_smallest_scale(cuda_device, past, new, group, t
     # where the weight of the zeros leaves less than 2^-126, bf16's steps are 2^-133 whatever the value: half a step of that
     assert ((got - want).abs() <= tol + 2.0 ** -134).all()
     assert (got != 0).any()
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("past,new,group", [([0, 0], [1, 1], 4), ([60, 0], [1, 2], 12), ([9000, 16], [1, 1], 4), ([70, 0], [60, 40], 2), ([6000, 100], [100, 130], 4)])
+def test_attention_of_infinite_queries(cuda_device, past, new, group, sign):
+    """An infinity in a query makes each score that the row sees infinite: of one sign (-infinity for all of them, too) or NaN where
+    the key is zero.  All that is NaN in the result, but zeros for a row that sees nothing, and no other row is touched."""
+    p = Plan(past, new, 2, 64, 16, seed=sum(past))
+    q = normal(p.T, 2 * group, 64, key=sum(new))
+    p.lensd[1] = 0 if past[1] == 0 else p.lensd[1]
+    base = attend(p, q, max_new=max(new))
+    p.kc[:] = torch.where(p.kc & 7 == 0, p.kc | 1, p.kc) & 0x77               # no key code is negative
+    p.kc[:] = torch.where(p.kc & 0x70 == 0, p.kc | 0x10, p.kc)                # or zero
+    bad = q.clone()
+    hit = torch.zeros(p.T, 2 * group, dtype=torch.bool, device="cuda")
+    hit[0, 1] = hit[-1, 0] = hit[p.T // 2, group] = True
+    bad[hit, 7] = sign * float("inf")
+    out = attend(p, bad, max_new=max(new))
+    sees = torch.tensor([p.lensd.tolist()[0 if t < new[0] else 1] > 0 for t in range(p.T)], device="cuda")
+    assert torch.equal(out.isnan(), (hit & sees[:, None])[:, :, None].expand_as(out))
+    assert (out[~sees] == 0).all() and (base[~sees] == 0).all()
+    # zeros among the keys: NaN scores
+    p.kc.zero_()
+    attend(p, bad, max_new=max(new))
+
+
+def test_attention_of_infinite_queries_over_holes(cuda_device):
+    """A row is zero where its table names no page, whatever the query; NaN from the first page that it sees."""
+    for new in (1, 70):
+        p = Plan([100, 100], [new, new], 1, 64, 16, seed=new)
+        p.table[0, :] = -1
+        p.table[1, :3] = p.pages
+        p.kc.fill_(0x22)
+        q = normal(p.T, 4, 64, key=new)
+        base = attend(p, q, max_new=new)
+        q[:, 2, 9] = -float("inf")               # (the reference has no bound for such a row that sees nothing)
+        out = kq.mx_paged_attention(q, *p.args, max_new=new)
+        assert (out[:new] == 0).all() and out[new:, 2].isnan().all() and torch.equal(out[:, [0, 1, 3]], base[:, [0, 1, 3]])

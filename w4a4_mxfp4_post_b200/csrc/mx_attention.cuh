@@ -7,7 +7,7 @@
 // over the positions j of t's sequence that its mask leaves: j <= the
 // position of t (causal) or every j below the sequence's length.  Positions
 // whose page the table does not name are not seen.  A row that sees nothing
-// is zero.
+// is zero, one that sees nothing but scores of -infinity NaN.
 //
 // Work.  The query heads of a kv head and the new tokens of a sequence are the
 // rows of one product over that head's cache: row r of (sequence b, kv head h)
@@ -52,7 +52,8 @@ struct Desc {
     int parts;
     int h, r0;                               // kv head, first row
     int lo, rows;                            // the sequence's first row of the call, its rows
-    int pad[3];
+    int b;                                   // sequence
+    int pad[2];
 };
 
 // Slot i of a workspace for R rows: output [D / 4][R][4] (a thread per row writes
@@ -237,6 +238,22 @@ __device__ __forceinline__ int64_t strip_row(const Args &a, const int32_t *table
     const int p = __ldg(table + j);
     if (p < 0 || p >= a.s.num_pages) return -1;
     return (int64_t(p) * a.s.heads + h) * a.s.page + (t - j * a.s.page);
+}
+
+// What a row of sequence b with a sum of zero is divided by the sum to: it saw
+// nothing (zeros stay), or every score that it saw was -infinity (NaN).
+__device__ __noinline__ float empty_row(const int32_t *table, int page, int num_pages, int end)
+{
+    for (int j = 0; int64_t(j) * page < end; ++j) {
+        const int p = __ldg(table + j);
+        if (p >= 0 && p < num_pages) return __uint_as_float(0x7fc00000u);
+    }
+    return 0.0f;
+}
+
+__device__ __forceinline__ float empty_row(const Args &a, int b, int end)
+{
+    return empty_row(a.s.table + int64_t(b) * a.s.table_stride, a.s.page, a.s.num_pages, end);
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -843,8 +860,8 @@ few_kernel(const Args a)
                 x = fmaf(v.x, f, x);
                 y = fmaf(v.y, f, y);
             }
-            // (a row that has seen nothing has zeros: they stay)
-            const float inv = ll == 0.0f ? 0.5f : 0.5f / ll;
+            float inv = 0.5f / ll;
+            if (ll == 0.0f) inv = whole ? empty_row(a, p.b, row_end(a, q, row)) : 0.0f;
             x = x * inv * vscale;
             y = y * inv * vscale;
             if (nan_first[d / 32] < row_end(a, q, row)) x = y = __uint_as_float(0x7fc00000u);
@@ -862,7 +879,7 @@ few_kernel(const Args a)
         if (!whole && p.unit == 0 && threadIdx.x == 0) {
             // the item starts here and goes on: the shares up to the one with its last unit hold it
             const int64_t last = quotient(total * (blockIdx.x + 1), shares) - left + units - 1;
-            *desc = Desc{int(share_of(last, total, shares)) - int(blockIdx.x) + 1, p.h, r0, q.lo, q.rows, {}};
+            *desc = Desc{int(share_of(last, total, shares)) - int(blockIdx.x) + 1, p.h, r0, q.lo, q.rows, p.b, {}};
         }
         __syncthreads();
         left -= count + C::kItemCost;
@@ -919,7 +936,7 @@ merge_kernel(const Args a)
         }
 #pragma unroll
         for (int i = 16; i; i >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, i);
-        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+        const float inv = ll == 0.0f ? empty_row(a, d.b, row_end(a, load_seq(a, d.b), r0 + r)) : 1.0f / ll;
         for (int k = lane; k < d.parts; k += 32) weight[r][k] *= inv;
     }
     __syncthreads();

@@ -704,8 +704,8 @@ chunk_kernel(const Args a, long long budget)
                 const bool whole = walk.count == units;
                 float *sl = slot<R, D>(a, 2 * int(blockIdx.x) + (p.unit == 0 ? 1 : 0));
                 const int ir = i * kTile + row;                              // row of the item
-                // a row that has seen nothing has zeros (or NaN) in O: they stay
-                const float scale = l == 0.0f ? 1.0f : 1.0f / l;
+                float scale = 1.0f / l;
+                if (l == 0.0f) scale = whole && mine ? empty_row(a, p.b, sees) : 0.0f;
                 if (!whole && mine) {
                     const float lower = (lowered[warp] >> lane) & 1 ? kLower : 0.0f;
                     sl[R * D + ir] = m == -INFINITY ? m : fmaf(m, c, lower);
@@ -763,7 +763,7 @@ chunk_kernel(const Args a, long long budget)
                     const int64_t total = totals[0], shares = totals[1];
                     const int64_t end = quotient(total * (blockIdx.x + 1), shares) - walk.left + units - 1;
                     reinterpret_cast<Desc *>(a.work)[blockIdx.x] =
-                        Desc{int(share_of(end, total, shares)) - int(blockIdx.x) + 1, p.h, p.tile * R, q.lo, q.rows, {}};
+                        Desc{int(share_of(end, total, shares)) - int(blockIdx.x) + 1, p.h, p.tile * R, q.lo, q.rows, p.b, {}};
                 }
             }
             // A tile's arrivals must not run ahead of the segments.  Both tiles wait in every segment: a wait on
@@ -811,7 +811,7 @@ merge_many_kernel(const Args a)
         return mk == -INFINITY ? (lk == 0.0f ? 0.0f : lk) : lk * ex2(mk - mm);
     };
     for (int k = 0; k < d.parts; ++k) ll += weight(k);
-    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+    const float inv = ll == 0.0f ? empty_row(a, d.b, row_end(a, load_seq(a, d.b), d.r0 + r)) : 1.0f / ll;
     float4 x[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
