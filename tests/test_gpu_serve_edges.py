@@ -191,3 +191,12 @@ def test_attention_of_infinite_queries_over_holes(cuda_device):
         q[:, 2, 9] = -float("inf")               # (the reference has no bound for such a row that sees nothing)
         out = kq.mx_paged_attention(q, *p.args, max_new=new)
         assert (out[:new] == 0).all() and out[new:, 2].isnan().all() and torch.equal(out[:, [0, 1, 3]], base[:, [0, 1, 3]])
+
+
+@pytest.mark.parametrize("past,new,group", [([150], [1], 4), ([9000], [2], 8), ([200], [60], 4)])
+def test_attention_of_a_large_scale_over_small_scores(cuda_device, past, new, group):
+    """The scale is any finite number: 2^120 over products of 2^-150, whose scores are next to zero."""
+    p = Plan(past, new, 2, 64, 32, seed=11)
+    p.ks.copy_(torch.randint(60, 68, p.ks.shape, dtype=torch.uint8, device="cuda", generator=rng(11)))
+    q = (normal(p.T, 2 * group, 64, key=11).float() * 2.0 ** -100).bfloat16()
+    attend(p, q, scale=2.0 ** 120, max_new=max(new))

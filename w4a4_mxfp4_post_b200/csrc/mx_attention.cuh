@@ -269,6 +269,13 @@ __device__ __forceinline__ float pow2(int e)
     return e < -126 ? 0.0f : __uint_as_float(uint32_t(min(e, 128) + 127) << 23);
 }
 
+// x * 2^e for -253 <= e <= 127, where 2^e itself may be below fp32's normal numbers.
+__device__ __forceinline__ float times_pow2(float x, int e)
+{
+    const int most = max(e, -126);
+    return x * pow2(most) * pow2(e - most);
+}
+
 // ---------------------------------------------------------------------------
 // A few rows (R = 8 or 16): the cache streams through once.
 //
@@ -541,7 +548,7 @@ few_kernel(const Args a)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) cs[t][i] = a.scale_log2 * pow2(max(qe[t][i] - 127, -126));
+            for (int i = 0; i < 2; ++i) cs[t][i] = times_pow2(a.scale_log2, qe[t][i] - 127);
         int it = 0;
         for (int t0 = t_first; t0 < t_end; t0 += 32 * W, ++it) {
             gemv::cp_wait<ST - 2>();
@@ -602,7 +609,7 @@ few_kernel(const Args a)
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) cs[t][i] = a.scale_log2 * pow2(max(min(qe[t][i] + kref - 127, 127), -126));
+                            for (int i = 0; i < 2; ++i) cs[t][i] = times_pow2(a.scale_log2, min(qe[t][i] + kref - 127, 127));
                     }
                     vmax = __reduce_max_sync(0xffffffffu, vmax);
                     if (vmax > vtop) {
