@@ -1,10 +1,13 @@
 """The few-token operators' binding, without a GPU: what it packs for the library and what it refuses."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
 
 import w4a4_mxfp4_post_b200 as kq
+from w4a4_mxfp4_post_b200 import build as kbuild
 
 CPU = torch.device("cpu")
 P = ctypes.c_void_p
@@ -12,9 +15,7 @@ P = ctypes.c_void_p
 
 @pytest.fixture(scope="module")
 def L():
-    from w4a4_mxfp4_post_b200 import build
-
-    build.build()
+    kbuild.build()
     return kq.lib()
 
 
@@ -65,3 +66,59 @@ def test_attention_rows_end_before_32_bits(L):
     assert L.mx_attention_workspace(most, 2, 2, 64, 1) > 0
     for bad in ((1 << 31, 2, 2, 64, 0), (1 << 62, 1 << 62, 2, 64, 1), (4, 1 << 40, 2, 64, 1), (4, 1 << 17, 1 << 17, 64, 1)):
         assert L.mx_attention_workspace(*bad) == -1
+
+
+@pytest.fixture
+def compilers(monkeypatch, tmp_path):
+    """build() into tmp_path with compilers that only write their output; `failing` maps a compiler to what it raises."""
+    calls, failing = [], {}
+
+    def run(cmd, check):
+        name = os.path.basename(cmd[0])
+        calls.append(name)
+        if name in failing:
+            raise failing[name]
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write(name)
+
+    monkeypatch.setattr(kbuild.subprocess, "run", run)
+    monkeypatch.setattr(kbuild, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(kbuild, "binding_path", lambda: str(tmp_path / "binding.so"))
+    return calls, failing, tmp_path
+
+
+def test_build_makes_the_library_and_the_binding(compilers):
+    calls, _, tmp = compilers
+    assert kbuild.build() == kbuild.LIB and calls == ["nvcc", "g++"]
+    assert (tmp / "lib.so").read_text() == "nvcc" and (tmp / "binding.so").read_text() == "g++"
+    assert kbuild.build() == kbuild.LIB and len(calls) == 2                  # nothing is stale
+    kbuild.build(force=True)
+    assert len(calls) == 4
+
+
+@pytest.mark.parametrize("error", [subprocess.CalledProcessError(1, ["g++"]), FileNotFoundError("g++")], ids=["fails", "missing"])
+def test_build_makes_the_library_without_the_binding(compilers, error):
+    """The library needs nvcc alone: where the native part of the binding does not compile, it is left out, and no older one stays."""
+    calls, failing, tmp = compilers
+    (tmp / "binding.so").write_text("older")
+    failing["g++"] = error
+    with pytest.warns(UserWarning, match="left out"):
+        assert kbuild.build(force=True) == kbuild.LIB
+    assert (tmp / "lib.so").exists() and not (tmp / "binding.so").exists() and calls == ["nvcc", "g++"]
+
+
+def test_build_without_torch_metadata(compilers, monkeypatch):
+    from importlib.metadata import PackageNotFoundError
+
+    def no_metadata():
+        raise PackageNotFoundError("torch")
+
+    monkeypatch.setattr(kbuild, "binding_path", no_metadata)
+    with pytest.warns(UserWarning, match="left out"):
+        assert kbuild.build(force=True) == kbuild.LIB and compilers[2].joinpath("lib.so").exists()
+
+
+def test_build_fails_without_the_library(compilers):
+    compilers[1]["nvcc"] = subprocess.CalledProcessError(1, ["nvcc"])
+    with pytest.raises(subprocess.CalledProcessError):
+        kbuild.build(force=True)

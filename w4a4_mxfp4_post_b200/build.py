@@ -6,14 +6,17 @@ binding's native part ``kq_binding.<torch version>.so``.
 The library is a plain shared object with the C ABI of ``include/kroquant.h``;
 it is compiled with nvcc for sm_100a only and links the CUDA runtime
 statically, so loading it needs no torch and no GPU.  The native part of the
-binding is host code against torch's headers; where torch is not installed it
-is left out, and the Python binding does its calls.
+binding is host code against torch's headers and is built after the library.
+Where torch is not installed it is left out; where it does not compile (a torch
+without CUDA, no g++, no Python headers) it is left out with a warning.  The
+Python binding then does its calls.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -63,6 +66,8 @@ def build_binding(force: bool = False) -> str | None:
     deps = [src, os.path.join(INCLUDE, "kroquant.h"), os.path.abspath(__file__)]
     if not force and os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps):
         return out
+    if os.path.exists(out):
+        os.remove(out)                       # if this build fails, nothing older is loaded in its place
     torch_dir = os.path.dirname(spec.origin)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     tmp = out + ".tmp%d" % os.getpid()
@@ -76,15 +81,17 @@ def build_binding(force: bool = False) -> str | None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_binding(force)
-    if not force and not _stale():
-        return LIB
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [nvcc(), *NVCC_FLAGS, "-I", INCLUDE, *SOURCES, "-o", tmp]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    if force or _stale():
+        tmp = LIB + ".tmp%d" % os.getpid()
+        cmd = [nvcc(), *NVCC_FLAGS, "-I", INCLUDE, *SOURCES, "-o", tmp]
+        if verbose:
+            cmd.insert(1, "-Xptxas=-v")
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, LIB)
+    try:
+        build_binding(force)
+    except (subprocess.CalledProcessError, OSError, ImportError) as e:
+        warnings.warn(f"the binding's native part is left out, it could not be built: {e}")
     return LIB
 
 
