@@ -122,3 +122,30 @@ def test_build_fails_without_the_library(compilers):
     compilers[1]["nvcc"] = subprocess.CalledProcessError(1, ["nvcc"])
     with pytest.raises(subprocess.CalledProcessError):
         kbuild.build(force=True)
+
+
+@pytest.mark.parametrize("why", ["absent", "no metadata", "no binary"])
+def test_calls_without_the_native_binding(L, monkeypatch, tmp_path, why):
+    """Where it was not built or does not load, the Python binding does the calls: found out once, and said."""
+    from importlib.metadata import PackageNotFoundError
+
+    asked = []
+
+    def path():
+        asked.append(1)
+        if why == "no metadata":
+            raise PackageNotFoundError("torch")
+        if why == "no binary":
+            (tmp_path / "binding.so").write_text("not a shared object")
+        return str(tmp_path / "binding.so")
+
+    monkeypatch.setattr(kbuild, "binding_path", path)
+    monkeypatch.setattr(kq, "_native_module", None)
+    if why == "absent":
+        assert kq._native() is False
+    else:
+        with pytest.warns(UserWarning, match="does not load"):
+            assert kq._native() is False
+    assert kq._native() is False and len(asked) == 1
+    with pytest.raises(ValueError, match="CUDA"):            # as the Python binding says it
+        kq.mxf4_gemv(torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8))

@@ -607,22 +607,27 @@ _native_module = None
 
 def _native():
     """The binding's native part (csrc/binding.cpp), which does ordinary calls of the few-token
-    operators in one step and answers None to the others; False where it was not built."""
+    operators in one step and answers None to the others; False where it was not built or does not load."""
     global _native_module
     if _native_module is None:
         import importlib.machinery
         import importlib.util
+        import warnings
 
         from .build import binding_path
 
-        path = binding_path()
-        if not os.path.exists(path):
-            _native_module = False
-            return False
         L = lib()
-        loader = importlib.machinery.ExtensionFileLoader("kq_binding", path)
-        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("kq_binding", path, loader=loader))
-        loader.exec_module(module)
+        _native_module = False
+        try:
+            path = binding_path()
+            if not os.path.exists(path):
+                return False
+            loader = importlib.machinery.ExtensionFileLoader("kq_binding", path)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("kq_binding", path, loader=loader))
+            loader.exec_module(module)
+        except (ImportError, OSError) as e:                  # (no metadata of torch, a file of another torch or Python)
+            warnings.warn(f"the binding's native part does not load, calls take longer: {e}")
+            return False
         module.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
             "mxf4_gemv", "mxf4_gemv_workspace", "kq_sf_bytes", "mx_cache_write", "mx_cache_read", "mx_paged_attention",
             "mx_attention_workspace")))
