@@ -2,6 +2,9 @@
 
 Inputs and 64-bit forms are those of test_gpu_serve.py and serve_ref.py.
 """
+import threading
+import time
+
 import pytest
 import torch
 
@@ -200,3 +203,39 @@ def test_attention_of_a_large_scale_over_small_scores(cuda_device, past, new, gr
     p.ks.copy_(torch.randint(60, 68, p.ks.shape, dtype=torch.uint8, device="cuda", generator=rng(11)))
     q = (normal(p.T, 2 * group, 64, key=11).float() * 2.0 ** -100).bfloat16()
     attend(p, q, scale=2.0 ** 120, max_new=max(new))
+
+
+# --- the binding ---------------------------------------------------------------
+
+def test_a_full_launch_queue_stops_no_other_thread(cuda_device, either_binding):
+    """A call whose launch waits for a place in the queue waits without the interpreter's lock."""
+    p = Plan([100], [1], 2, 64, 16, seed=3)
+    x = normal(1, 16, 64, key=3)
+    w, wsf = kq.mx_quantize_f32(torch.randn(64, 512, device="cuda"), sf_layout=True)
+    calls = [lambda: kq.mx_cache_write(x[:, :2], x[:, 2:4], *p.args), lambda: kq.mx_cache_read(*p.cache, p.table, p.cud, 1),
+             lambda: kq.mxf4_gemv(x.view(2, 512), w, wsf), lambda: kq.mx_paged_attention(x[:, 4:12], *p.args, max_new=1)]
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+        gaps, stop = [], threading.Event()
+
+        def ticks():
+            last = time.perf_counter()
+            while not stop.is_set():
+                time.sleep(0.001)
+                now = time.perf_counter()
+                gaps.append(now - last)
+                last = now
+
+        t = threading.Thread(target=ticks)
+        t.start()
+        torch.cuda._sleep(1_200_000_000)     # 0.6 s and more
+        begun = time.perf_counter()
+        for _ in range(2500):
+            call()
+        took = time.perf_counter() - begun
+        torch.cuda.synchronize()
+        stop.set()
+        t.join()
+        assert took > 0.3, "the queue did not fill"
+        assert max(gaps) < 0.2, f"another thread stood still for {max(gaps):.2f} s"

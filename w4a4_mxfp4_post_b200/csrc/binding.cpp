@@ -31,6 +31,16 @@ decltype(&mx_cache_read) p_read;
 decltype(&mx_paged_attention) p_attention;
 decltype(&mx_attention_workspace) p_attention_workspace;
 
+// Without the interpreter's lock, as ctypes calls: a launch waits where the queue is full.
+template <class F, class... A>
+int unlocked(F f, A... args)
+{
+    PyThreadState *state = PyEval_SaveThread();
+    const int rc = f(args...);
+    PyEval_RestoreThread(state);
+    return rc;
+}
+
 // The tensor of a Python argument; NULL if it is none (or of a subclass).
 const at::Tensor *tensor(PyObject *o) { return THPVariable_CheckExact(o) ? &THPVariable_Unpack(o) : nullptr; }
 
@@ -116,9 +126,9 @@ PyObject *gemv(PyObject *, PyObject *const *args, Py_ssize_t n)
     at::Tensor out = at::empty({M, N}, x->options().dtype(f32 ? at::kFloat : at::kBFloat16).requires_grad(false));
     at::Tensor work;
     if (need > 0) work = at::empty({need}, codes->options());
-    const int rc = p_gemv(x->data_ptr(), M > 1 ? x->stride(0) : K, static_cast<const uint8_t *>(codes->data_ptr()),
-                          static_cast<const uint8_t *>(sf->data_ptr()), out.data_ptr(), f32, M, N, K,
-                          need > 0 ? work.data_ptr() : nullptr, need, dev.stream());
+    const int rc = unlocked(p_gemv, x->data_ptr(), M > 1 ? x->stride(0) : K, static_cast<const uint8_t *>(codes->data_ptr()),
+                            static_cast<const uint8_t *>(sf->data_ptr()), out.data_ptr(), f32, M, N, K,
+                            need > 0 ? work.data_ptr() : nullptr, need, dev.stream());
     return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
 }
@@ -136,8 +146,8 @@ PyObject *write(PyObject *, PyObject *const *args, Py_ssize_t n)
     if (!rows_ok(k, dev, k->scalar_type(), c.head_dim) || !rows_ok(v, dev, k->scalar_type(), c.head_dim) ||
         k->size(1) != c.heads || v->sizes() != k->sizes())
         return none();
-    const int rc = p_write(k->data_ptr(), k->stride(0), k->stride(1), v->data_ptr(), v->stride(0), v->stride(1),
-                           k->scalar_type() == at::kFloat, &c, &b, k->size(0), dev.stream());
+    const int rc = unlocked(p_write, k->data_ptr(), k->stride(0), k->stride(1), v->data_ptr(), v->stride(0), v->stride(1),
+                            k->scalar_type() == at::kFloat, &c, &b, k->size(0), dev.stream());
     if (rc) return PyLong_FromLong(rc);
     Py_RETURN_TRUE;
     END_HANDLE_TH_ERRORS
@@ -164,8 +174,8 @@ PyObject *read(PyObject *, PyObject *const *args, Py_ssize_t n)
     const bool f32 = args[8] == Py_True;
     const auto options = THPVariable_Unpack(args[0]).options().dtype(f32 ? at::kFloat : at::kBFloat16);
     at::Tensor k = at::empty({T, c.heads, c.head_dim}, options), v = at::empty({T, c.heads, c.head_dim}, options);
-    const int rc = p_read(&c, &b, starts ? static_cast<const int32_t *>(starts->data_ptr()) : nullptr, k.data_ptr(),
-                          v.data_ptr(), f32, T, dev.stream());
+    const int rc = unlocked(p_read, &c, &b, starts ? static_cast<const int32_t *>(starts->data_ptr()) : nullptr, k.data_ptr(),
+                            v.data_ptr(), f32, T, dev.stream());
     if (rc) return PyLong_FromLong(rc);
     PyObject *pair = PyTuple_New(2);
     if (!pair) return nullptr;
@@ -207,8 +217,8 @@ PyObject *attention(PyObject *, PyObject *const *args, Py_ssize_t n)
     if (need < 0) return none();
     at::Tensor out = at::empty({T, hq, c.head_dim}, q->options().requires_grad(false));
     at::Tensor work = at::empty({need}, THPVariable_Unpack(args[1]).options());
-    const int rc = p_attention(q->data_ptr(), q->stride(0), q->stride(1), &c, &b, float(scale), args[10] != Py_False,
-                               out.data_ptr(), T, hq, max_new, work.data_ptr(), need, dev.stream());
+    const int rc = unlocked(p_attention, q->data_ptr(), q->stride(0), q->stride(1), &c, &b, float(scale), args[10] != Py_False,
+                            out.data_ptr(), T, hq, max_new, work.data_ptr(), need, dev.stream());
     return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
 }
