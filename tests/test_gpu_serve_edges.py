@@ -239,3 +239,29 @@ def test_a_full_launch_queue_stops_no_other_thread(cuda_device, either_binding):
         t.join()
         assert took > 0.3, "the queue did not fill"
         assert max(gaps) < 0.2, f"another thread stood still for {max(gaps):.2f} s"
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+@pytest.mark.parametrize("op", ["gemv", "read", "attention"])
+def test_results_of_another_stream_take_no_memory_of_the_current_one(cuda_device, op, raw):
+    """Memory freed on the current stream is still read there; a call on another stream must not write it."""
+    side = torch.cuda.Stream()
+    p = Plan([0], [4096], 8, 128, 64, seed=4)
+    x = normal(4096, 32, 128, key=4)
+    w, wsf = kq.mx_quantize_f32(torch.randn(40000, 512, device="cuda"), sf_layout=True)
+    call = {"gemv": lambda s: kq.mxf4_gemv(x.view(-1, 512)[:32], w, wsf, out_dtype=torch.float32, stream=s),
+            "read": lambda s: kq.mx_cache_read(*p.cache, p.table, p.cud, 4096, stream=s)[0],
+            "attention": lambda s: kq.mx_paged_attention(x, *p.args, max_new=4096, stream=s)}[op]
+    want = call(None)
+    call(side)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    used = torch.full_like(want, 3.0)
+    torch.cuda._sleep(200_000_000)           # 0.1 s: the copy below is still to come
+    copy = used.clone()
+    del used
+    out = call(side.cuda_stream if raw else side)
+    side.synchronize()
+    assert torch.equal(out, want)
+    torch.cuda.synchronize()
+    assert (copy == 3).all()

@@ -573,6 +573,8 @@ def mxf4_gemv(x, b_codes, b_sf, out=None, out_dtype=None, workspace=None, stream
     x bf16 [M, K] (rows may be strided), not quantized; b_codes [N, K/2] and b_sf the
     weight operand of mxf4_gemm; out bf16 (default) or float32 [M, N].  workspace: uint8
     tensor of mxf4_gemv_workspace(M, N, K) bytes for this call alone; allocated if None.
+    stream: default the current one; what a call on another allocates (results, too) is that
+    stream's, as under torch.cuda.stream(stream).
     """
     torch = _torch()
     if out is None and workspace is None and stream is None and (out_dtype is None or out_dtype in (torch.bfloat16, torch.float32)):
@@ -585,7 +587,7 @@ def mxf4_gemv(x, b_codes, b_sf, out=None, out_dtype=None, workspace=None, stream
     K = x.shape[1]
     dev = x.device
     if out is None:
-        out = x.new_empty((M, N), dtype=out_dtype)
+        out = _new((M, N), out_dtype or torch.bfloat16, dev, stream)
     else:
         _need(out, "out", out.dtype, dev, (M, N))
     f32 = out.dtype is torch.float32
@@ -595,7 +597,7 @@ def mxf4_gemv(x, b_codes, b_sf, out=None, out_dtype=None, workspace=None, stream
     if workspace is not None:
         _need(workspace, "workspace", u8, dev)
     elif need > 0:
-        workspace = _scratch(need, dev, stream)
+        workspace = _new((need,), u8, dev, stream)
     _call("mxf4_gemv", dev, x.data_ptr(), x.stride(0) if M > 1 else K, b_codes.data_ptr(), b_sf.data_ptr(), out.data_ptr(),
           f32, M, N, K,
           _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, dev))
@@ -782,7 +784,8 @@ def mx_cache_read(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens,
     """Positions of a paged MXFP4 cache back as bf16 (default) or float32, keys and values.
 
     Row cu_seqlens[b] + i of the [rows, heads, head_dim] outputs is position starts[b] + i
-    (starts int32 [B], default zeros) of sequence b.
+    (starts int32 [B], default zeros) of sequence b.  Rows of no sequence keep their values
+    (undefined ones where the call allocates the outputs).  stream as in mxf4_gemv.
     """
     torch = _torch()
     if out_k is None and out_v is None and stream is None and (out_dtype is None or out_dtype in (torch.bfloat16, torch.float32)):
@@ -801,11 +804,11 @@ def mx_cache_read(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens,
     if not f32 and dtype is not torch.bfloat16:
         raise TypeError(f"out_k and out_v must be bfloat16 or float32, got {dtype}")
     if out_k is None:
-        out_k = k_codes.new_empty(shape, dtype=dtype)
+        out_k = _new(shape, dtype, dev, stream)
     else:
         _need(out_k, "out_k", dtype, dev, shape)
     if out_v is None:
-        out_v = torch.empty_like(out_k)
+        out_v = _new(shape, dtype, dev, stream)
     else:
         _need(out_v, "out_v", dtype, dev, shape)
     _call("mx_cache_read", dev, c, b, _ptr(starts), out_k.data_ptr(), out_v.data_ptr(), f32, shape[0], _stream(stream, dev))
@@ -828,8 +831,9 @@ def mx_paged_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_
     cache's heads.  The new tokens' keys and values have been written (mx_cache_write).
     causal: a token sees the positions up to its own, otherwise all seq_lens[b].  scale:
     default head_dim ** -0.5.  max_new: the most new tokens of any one sequence, if known.
-    out bf16 [T, heads_q, head_dim]; rows of no sequence keep their values.  workspace: uint8
-    tensor of mx_attention_workspace(...) bytes for this call alone; allocated if None.
+    out bf16 [T, heads_q, head_dim]; rows of no sequence keep their values (undefined ones
+    where the call allocates it).  workspace: uint8 tensor of mx_attention_workspace(...) bytes
+    for this call alone; allocated if None.  stream as in mxf4_gemv.
     """
     torch = _torch()
     if out is None and workspace is None and stream is None:
@@ -849,12 +853,12 @@ def mx_paged_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_
     max_new = T if max_new is None else int(max_new)
     scale = d ** -0.5 if scale is None else float(scale)
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _new(shape, torch.bfloat16, dev, stream)
     else:
         _need(out, "out", torch.bfloat16, dev, shape)
     if workspace is None:
         need = mx_attention_workspace(T, hq, H, d, max_new)
-        workspace = _scratch(need, dev, stream)
+        workspace = _new((need,), torch.uint8, dev, stream)
     else:
         _need(workspace, "workspace", torch.uint8, dev)
         need = workspace.numel()
@@ -864,13 +868,13 @@ def mx_paged_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_
     return out
 
 
-def _scratch(nbytes, device, stream):
-    """Memory for one call: of the pool of the stream that the call runs on, so that it is
-    used again only after the call."""
+def _new(shape, dtype, device, stream):
+    """Memory for a call: of the pool of the stream that the call runs on, so that what used it
+    before and what uses it afterwards is in that stream's order."""
     torch = _torch()
     if stream is None:
-        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device)
     with torch.cuda.stream(stream):
-        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
