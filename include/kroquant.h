@@ -328,7 +328,7 @@ typedef struct {
  * mx_quantize_f32's for fp32: e.g. keys that kq_transform_f32 transformed).
  * k, v: bf16 or (in_f32 != 0) float32 [T][heads][head_dim], token and head
  * strides in elements, so slices of a fused projection do; 16-byte aligned,
- * strides whole 16-byte pieces.  A block with a value that is not finite is
+ * strides whole 16-byte pieces (not read for one token or head).  A block with a value that is not finite is
  * written as the NaN scale 0xFF with zero codes.  Positions other than the new
  * tokens' keep their bytes.  Two new tokens at the same place of the pool (two
  * sequences whose new tokens share a page) are outside the contract: its

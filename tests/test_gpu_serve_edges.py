@@ -265,3 +265,16 @@ def test_results_of_another_stream_take_no_memory_of_the_current_one(cuda_device
     assert torch.equal(out, want)
     torch.cuda.synchronize()
     assert (copy == 3).all()
+
+
+def test_one_token_or_head_with_any_stride(cuda_device, either_binding):
+    """Strides of dimensions of size 1 are not used, whatever the tensor says."""
+    for H, new, st, sh in ((2, 1, 1331, None), (1, 3, None, 7), (1, 1, 5, 3)):
+        p = Plan([20], [new], H, 64, 16, seed=6)
+        k, v, q = (normal(new, H, 64, key=i) for i in (1, 2, 3))
+        odd = [t.as_strided(t.shape, (st or t.stride(0), sh or t.stride(1), 1)) for t in (k, v, q)]
+        copies = [[t.clone() for t in p.cache] for _ in range(2)]
+        kq.mx_cache_write(k, v, *copies[0], p.table, p.cud, p.lensd)
+        kq.mx_cache_write(*odd[:2], *copies[1], p.table, p.cud, p.lensd)
+        assert all(torch.equal(a, b) for a, b in zip(*copies))
+        assert torch.equal(kq.mx_paged_attention(odd[2], *p.args, max_new=new), kq.mx_paged_attention(q, *p.args, max_new=new))

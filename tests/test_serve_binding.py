@@ -149,3 +149,17 @@ def test_calls_without_the_native_binding(L, monkeypatch, tmp_path, why):
     assert kq._native() is False and len(asked) == 1
     with pytest.raises(ValueError, match="CUDA"):            # as the Python binding says it
         kq.mxf4_gemv(torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8))
+
+
+def test_strides_of_one_token_or_head_are_not_read(L):
+    """The stride of a dimension of size 1 may be anything: these calls fail the check behind the strides'."""
+    seqs = kq._BATCH.pack(16, 3, 3, 16, 16, 2)
+    one, two = (kq._CACHE.pack(16, 16, 16, 16, 4, heads, 16, 64) for heads in (1, 2))
+    for cache, T, st, sh in ((two, 1, 132, 64), (two, 1, -1, 64), (one, 4, 128, 3), (one, 1, 1, 1)):
+        assert L.mx_cache_write(P(16), st, sh, None, st, sh, 0, cache, seqs, T, None) == -1
+        assert L.mx_cache_write(P(16), 128, 64, P(8), st, sh, 0, cache, seqs, T, None) == -3
+        heads = 1 if cache == one else 4
+        assert L.mx_paged_attention(P(16), st, sh, cache, seqs, 1.0, 1, None, T, heads, 1, P(16), 1 << 40, None) == -1
+    for cache, T, st, sh in ((two, 2, 132, 64), (two, 1, 128, 3), (one, 2, 132, 64)):
+        assert L.mx_cache_write(P(16), st, sh, None, 128, 64, 0, cache, seqs, T, None) == -3
+        assert L.mx_paged_attention(P(16), st, sh, cache, seqs, 1.0, 1, None, T, 4, 1, P(16), 1 << 40, None) == -3

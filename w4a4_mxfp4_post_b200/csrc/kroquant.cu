@@ -2736,10 +2736,13 @@ int check_seq_pointers(const char *fn, const mx_cache *c, const mx_batch *b, boo
 }
 
 // A strided [T][heads][D] operand: strides of a token and a head in elements,
-// each a whole number of 16-byte pieces.
-int check_strided(const char *fn, const char *what, const void *p, int64_t st, int64_t sh, int elem)
+// each a whole number of 16-byte pieces (those of a single token or head may be
+// anything: they are not used).
+int check_strided(const char *fn, const char *what, const void *p, int64_t T, int64_t heads, int64_t st, int64_t sh, int elem)
 {
     if (!p) return fail(KQ_ERR_NULL, "%s: NULL pointer argument (%s)", fn, what);
+    if (T <= 1) st = 0;
+    if (heads <= 1) sh = 0;
     if (st < 0 || sh < 0) return fail(KQ_ERR_SHAPE, "%s: strides of %s must not be negative", fn, what);
     if (!aligned(p, 16) || (st * elem) % 16 != 0 || (sh * elem) % 16 != 0)
         return fail(KQ_ERR_ALIGN, "%s: %s must be 16-byte aligned with strides of whole 16-byte pieces", fn, what);
@@ -3431,8 +3434,8 @@ int mx_cache_write(const void *k, int64_t k_stride_t, int64_t k_stride_h, const 
     if (T == 0 || b->batch == 0 || c->num_pages == 0 || b->max_pages == 0) return ok();
     const int elem = in_f32 ? 4 : 2;
     if ((rc = check_seq_pointers(fn, c, b, true)) != KQ_OK) return rc;
-    if ((rc = check_strided(fn, "k", k, k_stride_t, k_stride_h, elem)) != KQ_OK) return rc;
-    if ((rc = check_strided(fn, "v", v, v_stride_t, v_stride_h, elem)) != KQ_OK) return rc;
+    if ((rc = check_strided(fn, "k", k, T, c->heads, k_stride_t, k_stride_h, elem)) != KQ_OK) return rc;
+    if ((rc = check_strided(fn, "v", v, T, c->heads, v_stride_t, v_stride_h, elem)) != KQ_OK) return rc;
     switch (c->head_dim / kBlk) {
     case 1: return cache_write<1>(fn, k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, in_f32 != 0, c, s, stream);
     case 2: return cache_write<2>(fn, k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, in_f32 != 0, c, s, stream);
@@ -3490,7 +3493,7 @@ int mx_paged_attention(const void *q_bf16, int64_t q_stride_t, int64_t q_stride_
     if (!std::isfinite(scale_log2)) return fail(KQ_ERR_SHAPE, "%s: scale must be finite, also times log2(e)", fn);
     if (T == 0 || b->batch == 0) return ok();
     if ((rc = check_seq_pointers(fn, c, b, true)) != KQ_OK) return rc;
-    if ((rc = check_strided(fn, "q", q_bf16, q_stride_t, q_stride_h, 2)) != KQ_OK) return rc;
+    if ((rc = check_strided(fn, "q", q_bf16, T, heads_q, q_stride_t, q_stride_h, 2)) != KQ_OK) return rc;
     if (!out_bf16) return fail(KQ_ERR_NULL, "%s: NULL pointer argument", fn);
     if (!aligned(out_bf16, 16)) return fail(KQ_ERR_ALIGN, "%s: out must be 16-byte aligned", fn);
     const int64_t need = mx_attention_workspace(T, heads_q, c->heads, c->head_dim, max_new);
