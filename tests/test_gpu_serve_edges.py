@@ -278,3 +278,47 @@ def test_one_token_or_head_with_any_stride(cuda_device, either_binding):
         kq.mx_cache_write(*odd[:2], *copies[1], p.table, p.cud, p.lensd)
         assert all(torch.equal(a, b) for a, b in zip(*copies))
         assert torch.equal(kq.mx_paged_attention(odd[2], *p.args, max_new=new), kq.mx_paged_attention(q, *p.args, max_new=new))
+
+
+# --- batches -------------------------------------------------------------------
+
+@pytest.mark.parametrize("B", [63, 64, 65, 127, 128, 129, 300])
+@pytest.mark.parametrize("group", [4, 12])
+def test_attention_of_large_batches_of_single_tokens(cuda_device, B, group):
+    """As many sequences as threads that divide the work, fewer and more, ragged, some without tokens or length."""
+    past = [(37 * b * b) % 211 for b in range(B)]
+    new = [0 if b % 11 == 5 else 1 for b in range(B)]
+    past[B // 2], past[B - 2] = 3000, 1700
+    p = Plan(past, new, 2, 32, 16, seed=B)
+    p.lensd[7] = 0
+    attend(p, normal(p.T, 2 * group, 32, key=B), max_new=1)
+
+
+@pytest.mark.parametrize("B", [129, 256, 257, 511, 513, 700])
+def test_attention_of_large_batches_with_chunks(cuda_device, B):
+    """Both kernels at once over such batches: sequences with more rows than the few-rows kernel takes beside single tokens."""
+    past = [(53 * b * b) % 157 for b in range(B)]
+    new = [(1, 7, 0, 2, 13)[b % 5] for b in range(B)]
+    past[B // 3], new[B // 3] = 2500, 40
+    p = Plan(past, new, 1, 32, 16, seed=B, pad=2)
+    attend(p, normal(p.T, 8, 32, key=B), max_new=max(new))
+    assert kq.kq_wait_timeouts() == 0
+
+
+def test_cache_of_a_large_batch(cuda_device):
+    """A single token for each of 1000 sequences, written and read back."""
+    B = 1000
+    p = Plan([b % 70 for b in range(B)], [1] * B, 2, 64, 16, seed=12)
+    x = normal(B, 4, 64, key=12)
+    kq.mx_cache_write(x[:, :2], x[:, 2:], *p.args)
+    starts = torch.tensor(p.past, dtype=torch.int32, device="cuda")
+    for got, src in zip(kq.mx_cache_read(*p.cache, p.table, p.cud, B, starts=starts), (x[:, :2], x[:, 2:])):
+        codes, scales = kq.mx_quantize(src.reshape(2 * B, 64).contiguous())
+        assert torch.equal(got.double(), ref.decode(codes, scales).view(B, 2, 64))
+
+
+def test_chunks_repeat_bit_for_bit(cuda_device):
+    p = Plan([3000, 20, 900], [90, 300, 1], 2, 128, 64, seed=13)
+    q = normal(p.T, 16, 128, key=13)
+    a = kq.mx_paged_attention(q, *p.args, max_new=300)
+    assert all(torch.equal(a, kq.mx_paged_attention(q, *p.args, max_new=300)) for _ in range(4))
