@@ -61,8 +61,9 @@ constexpr int kRing = 2;                                     // steps of K and o
 constexpr int kDecodeWarps = 7;
 constexpr int kMmaWarp = kSoftmaxWarps + kDecodeWarps;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
-// Registers a thread: 128 at launch, some moved to the softmax warpgroups.
-constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;
+// Registers a thread: 128 at launch, some moved to the softmax warpgroups.  144 and 112, 152 and 104, 160 and 96: 512
+// tokens after 30000 257, 260 and 258 us, 4096 fresh ones 194, 198 and 198.
+constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;
 static_assert(kSoftmaxWarps % 4 == 0, "the split goes by whole warpgroups");
 static_assert(kThreads == 512 && 256 * (kSoftmaxRegs + kOtherRegs) <= 512 * 128, "the split stays within the launch's registers");
 constexpr int kSegs = 2 * kRing;                             // segments whose NaN positions are kept
