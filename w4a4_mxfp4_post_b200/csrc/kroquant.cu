@@ -2848,7 +2848,7 @@ int gemv_launch(const char *fn, const GemvArgs &a, int parts, int S)
     return launch_check(fn);
 }
 
-// Row tiles of 8 rows for M rows, 0 for M = 0.
+// Row tiles of 8 rows that the kernel takes for M rows.
 int gemv_tiles(int64_t M) { return M <= 8 ? 1 : M <= 16 ? 2 : 4; }
 
 bool gemv_pre(int64_t M, int64_t N, int64_t K)

@@ -12,6 +12,24 @@
 // device arrays say is bounded here before it is used, so a plan that is
 // wrong costs rows, never an access out of bounds.
 
+__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Eight codes as bf16 pairs (0,4) (1,5) (2,6) (3,7), times the pair f: one AND,
+// one multiply and one AND put codes n and n + 4 side by side as bf16 numbers
+// code * 2^-126 (code 1, 0.5, is a subnormal).
+__device__ __forceinline__ uint4 codes8_bf16(uint32_t w, uint32_t f)
+{
+    constexpr uint32_t kA = (1u << 12) + (1u << 6), kB = (1u << 8) + (1u << 2), kM = 0x81C081C0u;
+    const uint32_t v = w >> 8;
+    return make_uint4(hmul2_bf16(((w & 0x000F000Fu) * kA) & kM, f), hmul2_bf16(((w & 0x00F000F0u) * kB) & kM, f),
+                      hmul2_bf16(((v & 0x000F000Fu) * kA) & kM, f), hmul2_bf16(((v & 0x00F000F0u) * kB) & kM, f));
+}
+
 namespace cache {
 
 // The device arrays of a call's sequences (mx_batch of the header).
@@ -103,23 +121,13 @@ struct Lane {
 // two factors, for bf16 takes code * 2^-126 to at most code * 2 in one.)
 __device__ __forceinline__ uint4 decode_bf16(uint32_t w, uint32_t sb)
 {
-    auto mul = [](uint32_t a, uint32_t b) {
-        uint32_t r;
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
-    };
-    // one AND, one multiply and one AND put codes n and n + 4 side by side as bf16 numbers code * 2^-126
-    constexpr uint32_t kA = (1u << 12) + (1u << 6), kB = (1u << 8) + (1u << 2), kM = 0x81C081C0u;
-    const uint32_t f = (min(sb, 128u) + 126u) * 0x00800080u, v = w >> 8;
-    uint32_t x[4] = {mul(((w & 0x000F000Fu) * kA) & kM, f), mul(((w & 0x00F000F0u) * kB) & kM, f),
-                     mul(((v & 0x000F000Fu) * kA) & kM, f), mul(((v & 0x00F000F0u) * kB) & kM, f)};
+    uint4 x = codes8_bf16(w, (min(sb, 128u) + 126u) * 0x00800080u);
     if (sb > 128u) {
         const uint32_t f2 = sb == 255u ? 0x7fc07fc0u : (sb - 1u) * 0x00800080u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = mul(x[i], f2);
+        x = make_uint4(hmul2_bf16(x.x, f2), hmul2_bf16(x.y, f2), hmul2_bf16(x.z, f2), hmul2_bf16(x.w, f2));
     }
-    return make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[0], x[1], 0x7632),
-                      __byte_perm(x[2], x[3], 0x7632));
+    return make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.z, x.w, 0x5410), __byte_perm(x.x, x.y, 0x7632),
+                      __byte_perm(x.z, x.w, 0x7632));
 }
 
 // Quantize the keys and values of new tokens into the cache, as the other MXFP4

@@ -211,15 +211,6 @@ __device__ __forceinline__ void load_piece(Piece<NB> &p, const uint8_t *__restri
     }
 }
 
-// Eight codes to bf16 pairs (0,4) (1,5) (2,6) (3,7), times f.
-__device__ __forceinline__ uint4 decode8(uint32_t w, uint32_t f)
-{
-    constexpr uint32_t kA = (1u << 12) + (1u << 6), kB = (1u << 8) + (1u << 2), kM = 0x81C081C0u;
-    const uint32_t v = w >> 8;
-    return make_uint4(hmul2_bf16(((w & 0x000F000Fu) * kA) & kM, f), hmul2_bf16(((w & 0x00F000F0u) * kB) & kM, f),
-                      hmul2_bf16(((v & 0x000F000Fu) * kA) & kM, f), hmul2_bf16(((v & 0x00F000F0u) * kB) & kM, f));
-}
-
 // A position into row `row` of the step at `dst`.  NaN blocks become NaN for
 // keys and zeros for values, whose NaN is put into the result.
 template <int NB>
@@ -241,10 +232,10 @@ __device__ __forceinline__ void decode_row(const Piece<NB> &p, uint32_t dst, int
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const uint32_t f = (((p.s >> (8 * b)) & 0xffu) + 126u) * 0x00800080u;
-            put(4 * b, decode8(p.c[b].x, f));
-            put(4 * b + 1, decode8(p.c[b].y, f));
-            put(4 * b + 2, decode8(p.c[b].z, f));
-            put(4 * b + 3, decode8(p.c[b].w, f));
+            put(4 * b, codes8_bf16(p.c[b].x, f));
+            put(4 * b + 1, codes8_bf16(p.c[b].y, f));
+            put(4 * b + 2, codes8_bf16(p.c[b].z, f));
+            put(4 * b + 3, codes8_bf16(p.c[b].w, f));
         }
     } else {
 #pragma unroll
@@ -256,7 +247,7 @@ __device__ __forceinline__ void decode_row(const Piece<NB> &p, uint32_t dst, int
                 f2 = keys ? 0x7fc07fc0u : 0u;
             }
             auto twice = [&](uint32_t w) {
-                const uint4 v = decode8(w, f);
+                const uint4 v = codes8_bf16(w, f);
                 return make_uint4(hmul2_bf16(v.x, f2), hmul2_bf16(v.y, f2), hmul2_bf16(v.z, f2), hmul2_bf16(v.w, f2));
             };
             put(4 * b, twice(p.c[b].x));
