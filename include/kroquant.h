@@ -311,7 +311,7 @@ typedef struct {
  *               which are its last ones: row cu[b] + i is at position
  *               seq_lens[b] - (cu[b+1] - cu[b]) + i.
  *   block_table int32 [batch] rows of max_pages entries, table_stride
- *               entries apart: position p of sequence b is in page
+ *               (>= max_pages) entries apart: position p of sequence b is in page
  *               block_table[b][p / page_size].  An entry outside
  *               [0, num_pages) is no page.
  * The values are bounded on the device: a position before 0, behind the
@@ -355,7 +355,9 @@ int mx_cache_read(const mx_cache *cache, const mx_batch *seqs, const int32_t *st
  * mx_cache_write); out bf16 [T][heads_q][head_dim], contiguous.  Scores,
  * maxima and sums in fp32; for the second product the probabilities are
  * rounded to bf16, or (few rows) multiplied by their values' scale and rounded
- * to fp16: half a step of it, or 2^-40 of the largest value scale times 6.  A position on no page is not seen; a row that sees nothing is
+ * to fp16: half a step of it, or 2^-40 of the largest value scale (of those
+ * that any of the sequence's rows sees) times 6.  Any value scales up to 252
+ * do: no intermediate is past fp32's range where the result is within it.  A position on no page is not seen; a row that sees nothing is
  * zero (one whose every score is -infinity NaN, as the formula has it); what a row does not see does not reach it, NaN or not.  K and V scale
  * bytes 253 to 255 (mx_cache_write writes none of the first two) read as NaN.
  * max_new: a bound on the new tokens of any one sequence (T does); it selects

@@ -830,7 +830,9 @@ def mx_paged_attention(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_
     q bf16 [T, heads_q, head_dim] (tokens and heads may be strided); heads_q a multiple of the
     cache's heads.  The new tokens' keys and values have been written (mx_cache_write).
     causal: a token sees the positions up to its own, otherwise all seq_lens[b].  scale:
-    default head_dim ** -0.5.  max_new: the most new tokens of any one sequence, if known.
+    default head_dim ** -0.5.  max_new: the most new tokens of any one sequence; T if left out,
+    which costs a batch of single tokens: with more than 48 rows per kv head (T times heads_q /
+    heads) the kernels for chunks are launched, too, for nothing.
     out bf16 [T, heads_q, head_dim]; rows of no sequence keep their values (undefined ones
     where the call allocates it).  workspace: uint8 tensor of mx_attention_workspace(...) bytes
     for this call alone; allocated if None.  stream as in mxf4_gemv.

@@ -310,13 +310,22 @@ __device__ __forceinline__ float times_pow2(float x, int e)
 // ring of stages (32 positions of keys, values and scales); a warp takes every
 // fourth stage of the share and waits for nothing but its own copies.  They
 // meet when an item ends.  Three CTAs to an SM: with four (128 registers) the
-// shares get shorter and 16 x 40000 takes 199 us instead of 176.
+// shares get shorter (16 x 40000 took 199 us where three took 176, two steps ago).
+//
+// Outputs are kept relative to the largest value scale that the warp has seen and
+// leave the kernel divided by their sum: neither 2^15 nor a sum over many
+// positions takes values near the end of the format's range past fp32.
 //
 // Measured, 64 query heads over 8 of 128 channels: 16 sequences of 27 to 40
-// thousand positions 166 us, 3.6 TB/s (0.55 of the copy bandwidth); 32 of 2.7 to
-// 4 thousand 47 us.  Issue slots 54 % and ALU 51 % busy at 2.7 warps per
+// thousand positions 165 us, 3.6 TB/s (0.55 of the copy bandwidth); 32 of 2.7 to
+// 4 thousand 48 us.  Issue slots 54 % and ALU 51 % busy at 2.7 warps per
 // scheduler: it is the instructions, some 670 per stage (1000 with values in
-// bf16, scales byte by byte and the maximum by shuffles), that bound it.
+// bf16, scales byte by byte and the maximum by shuffles), that bound it.  A quarter
+// of them unpack codes; about half are the stage's own (scales, votes, tables,
+// maxima, addresses) whatever the channels and rows: 32 x 4096 takes 34, 39, 46 and
+// 48 us with 32, 64, 96 and 128 channels.  With 9 to 16 rows (NT = 2) 128 channels
+// spill, and more than 16 rows are items that read the cache again: 16 x 8000 with
+// 32 rows 107 us, with 16 rows 67.
 template <int D_, int NT_>
 struct Few {
     static constexpr int D = D_, NT = NT_;

@@ -41,10 +41,11 @@
 // Every wait is bounded (g_wait_timeouts).
 //
 // Measured, 32 query heads over 8 of 128 channels: 2048 tokens over 32,048
-// positions 0.86 ms, 1.21 PFLOP/s (0.74 of a cuBLAS bf16 product's burst rate,
-// 0.87 of its sustained one); 512 over 8,512 81 us; a causal prompt of 4096
-// 165 us.  A step of both tiles takes 4050 clocks: tensor pipe and exponential
-// unit 47 % busy, issue slots 49 %.  A tile's turn is Q K' (some 700 clocks with
+// positions 0.93 ms in single replays, 1.12 PFLOP/s (0.68 of a cuBLAS bf16
+// product's burst rate), 1.00 ms one after the other (0.75 of its sustained one);
+// 512 over 8,512 88 us; a causal prompt of 4096 188 us.  A step of both tiles takes
+// some 4200 clocks: tensor pipe and exponential
+// unit 44 % busy, issue slots 50 %.  A tile's turn is Q K' (some 700 clocks with
 // P V before it), the softmax (3000, of which 2000 while the other tile's
 // exponentials compete), then P V.  An item costs some 12,000 clocks beside
 // its steps: 3,500 until its queries are in place, 1,500 until the first S,

@@ -41,10 +41,13 @@
 // through distributed shared memory in rank order: the same bits every time.
 //
 // Measured, 8192 x 28672 weights (125 MB; a cp.async loop that only reads them
-// takes 28 to 31 us): 1 row 34 us, 3.6 TB/s; 8 rows 38; 16 rows 51 (63 with x
-// converted in every CTA); 32 rows 77.  With 16 rows issue slots are 43 % and the
+// takes 28 to 31 us): 1 row 33 us, 3.7 TB/s; 8 rows 37; 16 rows 50 (63 with x
+// converted in every CTA); 32 rows 76.  With 16 rows issue slots are 45 % and the
 // tensor pipe 31 % busy, 3.4 warps to a scheduler: shared-memory reads of x (16
-// bytes for every 4 of codes) and the barrier per stage are in the way.
+// bytes for every 4 of codes) and the barrier per stage are in the way.  Small
+// products whose x is converted in every CTA convert more of it than they use:
+// a rank of 5 x 5600 x 2240 takes 2 or 3 of the 9 chunks and converts up to 8 (9 us,
+// of which a launch is 3).
 
 namespace gemv {
 
