@@ -357,7 +357,8 @@ int mx_cache_read(const mx_cache *cache, const mx_batch *seqs, const int32_t *st
  * rounded to bf16, or (few rows) multiplied by their values' scale and rounded
  * to fp16: half a step of it, or 2^-40 of the largest value scale (of those
  * that any of the sequence's rows sees) times 6.  Any value scales up to 252
- * do: no intermediate is past fp32's range where the result is within it.  A position on no page is not seen; a row that sees nothing is
+ * do: no sum of values is past fp32's range where the result is within it
+ * (q . k itself has to be within it, before the scale).  A position on no page is not seen; a row that sees nothing is
  * zero (one whose every score is -infinity NaN, as the formula has it); what a row does not see does not reach it, NaN or not.  K and V scale
  * bytes 253 to 255 (mx_cache_write writes none of the first two) read as NaN.
  * max_new: a bound on the new tokens of any one sequence (T does); it selects
